@@ -20,7 +20,10 @@ __all__ = ["DGError", "Params", "lib", "workspace_size", "Workspace", "denoise_s
            "noalloc_selftest_bounded_wait", "STATUS", "E_BF16", "E_FP8_E4M3",
            "SELECT_CUMSUM", "SELECT_MI", "SELECT_TOPK", "partials_count", "head_partials", "merge_partials",
            "gather_partials", "init_canvas", "generate_blocks", "loop_state_bytes", "LoopState",
-           "denoise_loop_graph", "selfcond_workspace_size", "embedder_transpose", "denoise_step_selfcond"]
+           "denoise_loop_graph", "selfcond_workspace_size", "embedder_transpose", "denoise_step_selfcond", "PAGE",
+           "ContextPlan", "context_plan", "context_status", "RopeFrequencies", "rope", "ContextCache",
+           "context_append", "context_workspace_size", "ContextWorkspace", "context_attention",
+           "generate_blocks_context"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdg.so")
@@ -30,7 +33,7 @@ E_FP8_E4M3 = 1
 
 STATUS = {0: "DG_OK", 1: "DG_ERR_INVALID_ARG", 2: "DG_ERR_UNSUPPORTED_SHAPE", 3: "DG_ERR_WORKSPACE",
           4: "DG_ERR_RANGE", 5: "DG_ERR_CUDA", 6: "DG_ERR_TIMEOUT", 7: "DG_ERR_CALLBACK",
-          8: "DG_ERR_NO_DEVICE", 9: "DG_ERR_VALUE"}
+          8: "DG_ERR_NO_DEVICE", 9: "DG_ERR_VALUE", 10: "DG_ERR_CAPACITY"}
 
 
 class DGError(RuntimeError):
@@ -49,6 +52,28 @@ class _Params(ctypes.Structure):
                 ("entropy_bound", ctypes.c_double), ("stop_entropy", ctypes.c_double),
                 ("seed", ctypes.c_uint64), ("selection_rule", ctypes.c_int32), ("top_k", ctypes.c_int32),
                 ("block", ctypes.c_int32)]
+
+
+class _Context(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int32), ("rows", ctypes.c_int32), ("pages", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in (
+                    "table", "held", "free_list", "free_count", "lens", "start", "positions", "slots", "runs",
+                    "free_next", "status")]
+
+
+class _Heads(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class _RopeArgs(ctypes.Structure):
+    _fields_ = [("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("magnitude", ctypes.c_float),
+                ("freq", ctypes.c_void_p)]
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("pages", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
+                ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p)]
 
 
 SELECT_CUMSUM = 0
@@ -142,6 +167,25 @@ def lib() -> ctypes.CDLL:
         L.dg_generate_blocks.argtypes = [ctypes.POINTER(_Shape), ctypes.POINTER(_Params), P, P, ctypes.c_int32,
                                          _BLOCK_HIDDEN_FN, P, P, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
         L.dg_generate_blocks.restype = ctypes.c_int
+        gb = list(L.dg_generate_blocks.argtypes)
+        L.dg_generate_blocks_context.argtypes = gb[:7] + [P, P] + gb[7:]
+        L.dg_generate_blocks_context.restype = ctypes.c_int
+        L.dg_context_plan.argtypes = [P, P, P, ctypes.c_int32, P]
+        L.dg_context_plan.restype = ctypes.c_int
+        L.dg_context_status.argtypes = [P, P]
+        L.dg_context_status.restype = ctypes.c_int
+        L.dg_rope_frequencies.argtypes = [ctypes.c_int32, ctypes.c_double, ctypes.c_int32, ctypes.c_double,
+                                          ctypes.c_int32, P, P]
+        L.dg_rope_frequencies.restype = ctypes.c_int
+        L.dg_rope.argtypes = [P, P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, P, P]
+        L.dg_rope.restype = ctypes.c_int
+        L.dg_context_append.argtypes = [P, P, P, P, P, P]
+        L.dg_context_append.restype = ctypes.c_int
+        L.dg_context_workspace_size.argtypes = [ctypes.c_int32] * 4
+        L.dg_context_workspace_size.restype = ctypes.c_size_t
+        L.dg_context_attention.argtypes = [P, P, P, P, ctypes.c_int32, ctypes.c_float, P, ctypes.c_int32,
+                                           ctypes.c_int32, P, P, ctypes.c_size_t, P]
+        L.dg_context_attention.restype = ctypes.c_int
         L.dg_partials_count.restype = ctypes.c_int32
         L.dg_partials_count.argtypes = [ctypes.POINTER(_Shape)]
         L.dg_head_partials.restype = ctypes.c_int
@@ -478,6 +522,24 @@ def generate_blocks(E, hidden_fn, n_blocks: int, h_buf, blocks, canvas, prev_arg
     ``blocks[:j]`` of the blocks committed so far.  ``blocks`` is an int32
     CUDA tensor [n_blocks, B*256].  Returns the host int32 array of steps
     taken, [n_blocks, B]."""
+    return _run_blocks(None, E, hidden_fn, n_blocks, h_buf, blocks, canvas, prev_argmax, accept, entropy, sampled,
+                       argmax, stop, ws, params, e_scale, stream)
+
+
+def generate_blocks_context(plan: ContextPlan, E, hidden_fn, n_blocks: int, h_buf, blocks, canvas, prev_argmax,
+                            accept, entropy, sampled, argmax, stop, ws: Workspace, params: Params = Params(),
+                            e_scale=None, stream=None):
+    """``generate_blocks`` with a context (``dg_generate_blocks_context``):
+    ``plan`` holds the tables of the block's provisional rows whenever
+    ``hidden_fn`` is called, for ``context_append`` and
+    ``context_attention``; the batch it held before the call is committed
+    first."""
+    return _run_blocks(plan, E, hidden_fn, n_blocks, h_buf, blocks, canvas, prev_argmax, accept, entropy, sampled,
+                       argmax, stop, ws, params, e_scale, stream)
+
+
+def _run_blocks(plan, E, hidden_fn, n_blocks, h_buf, blocks, canvas, prev_argmax, accept, entropy, sampled, argmax,
+                stop, ws, params, e_scale, stream):
     R, d = h_buf.shape
     B = int(len(stop))
     V = E.shape[0]
@@ -496,17 +558,251 @@ def generate_blocks(E, hidden_fn, n_blocks: int, h_buf, blocks, canvas, prev_arg
             return 1
 
     cfn = _BLOCK_HIDDEN_FN(cb)
-    code = lib().dg_generate_blocks(
-        ctypes.byref(shp), ctypes.byref(prm), _ptr(E), _ptr(e_scale), ctypes.c_int32(n_blocks), cfn, None,
-        _ptr(h_buf), _ptr(blocks), steps.ctypes.data_as(ctypes.c_void_p), _ptr(canvas), _ptr(prev_argmax),
-        _ptr(accept), _ptr(entropy), _ptr(sampled), _ptr(argmax), _ptr(stop), _ptr(ws.buf),
-        ctypes.c_size_t(ws.nbytes), _stream(stream))
+    head = (ctypes.byref(shp), ctypes.byref(prm), _ptr(E), _ptr(e_scale), ctypes.c_int32(n_blocks), cfn, None)
+    tail = (_ptr(h_buf), _ptr(blocks), steps.ctypes.data_as(ctypes.c_void_p), _ptr(canvas), _ptr(prev_argmax),
+            _ptr(accept), _ptr(entropy), _ptr(sampled), _ptr(argmax), _ptr(stop), _ptr(ws.buf),
+            ctypes.c_size_t(ws.nbytes), _stream(stream))
+    if plan is None:
+        where = "dg_generate_blocks"
+        code = lib().dg_generate_blocks(*head, *tail)
+    else:
+        where = "dg_generate_blocks_context"
+        code = lib().dg_generate_blocks_context(*head, plan._ref, _ptr(plan.add), *tail)
     if code != 0:
-        err = DGError(code, "dg_generate_blocks")
+        err = DGError(code, where)
         if errors:
             raise err from errors[0]
         raise err
     return steps
+
+
+# ---------------------------------------------------------------------------
+# the context of block-by-block generation: block tables, rotary positions,
+# the 8-bit paged cache and the attention over it
+# ---------------------------------------------------------------------------
+
+PAGE = 64  # token slots per page
+
+_ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
+
+
+def _need(ok: bool, what: str) -> None:
+    if not ok:
+        raise DGError(1, what)
+
+
+def _on(device, stream):
+    """The stream handle to launch on for tensors of ``device``."""
+    import torch
+    if stream is None:
+        return torch.cuda.current_stream(device).cuda_stream
+    _need(stream.device == device, "the stream belongs to another device than the tensors")
+    return stream.cuda_stream
+
+
+def _call(device, fn, where, *args):
+    """Call a library function with the tensors' device current."""
+    import torch
+    if torch.cuda.current_device() == device.index:
+        code = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            code = fn(*args)
+    if code != 0:
+        _check(code, where)
+
+
+def _heads(t, rows, heads, dim, device, name) -> _Heads:
+    import torch
+    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.device != device:
+        raise DGError(1, f"{name} must be a bfloat16 tensor [rows, heads, dim] on {device}")
+    n, h, d = t.shape
+    rs, hs, ds = t.stride()
+    if n < rows or h != heads or d != dim:
+        raise DGError(2, f"{name} must be [{rows} (or more), {heads}, {dim}], not {list(t.shape)}")
+    # the stride of a dimension of one element is not a property of the data
+    if h == 1:
+        hs = dim
+    if n == 1:
+        rs = max(rs if rs % 8 == 0 else 0, dim)
+    if ds != 1 or rs < dim or (h > 1 and hs < dim) or rs % 8 or hs % 8 or t.data_ptr() % 16:
+        raise DGError(1, f"{name} needs contiguous heads, strides of multiples of 8 elements and 16-byte alignment")
+    return _Heads(t.data_ptr(), rs, hs)
+
+
+class ContextPlan:
+    """The state of a context and the tables of its provisional batch
+    (``dg_context`` in include/dg.h), as int32 CUDA tensors (``slots`` int64):
+    ``table`` [B, max_pages], ``held`` [B], ``free_list`` [pages],
+    ``free_count`` [1]; results ``lens`` [B], ``start`` [B + 1], ``positions``
+    and ``slots`` [rows], ``runs`` [rows // 64 + 2 B, 4], ``free_next`` [1],
+    ``status`` [2].  A new plan is empty, all pages free."""
+
+    def __init__(self, B: int, rows: int, pages: int, max_pages: int, device=None):
+        import torch
+        _need(min(B, rows, pages, max_pages) >= 1, "ContextPlan sizes must be positive")
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.B, self.rows, self.pages, self.max_pages, self.device = int(B), int(rows), int(pages), int(max_pages), device
+
+        def zeros(*n, dtype=torch.int32):
+            return torch.zeros(n, dtype=dtype, device=device)
+        self.table = torch.full((B, max_pages), -1, dtype=torch.int32, device=device)
+        self.held, self.lens, self.start = zeros(B), zeros(B), zeros(B + 1)
+        self.free_list = torch.arange(pages, dtype=torch.int32, device=device)
+        self.free_count, self.free_next = zeros(1) + pages, zeros(1) + pages
+        self.positions, self.slots = zeros(rows) - 1, zeros(rows, dtype=torch.int64) - 1
+        self.runs = zeros(rows // PAGE + 2 * B, 4)
+        self.runs[:, 0] = -1
+        self.status = zeros(2)
+        self.add = zeros(B)  # lengths of generate_blocks_context
+        self._c = _Context(B, rows, pages, max_pages, *(getattr(self, n).data_ptr() for n in (
+            "table", "held", "free_list", "free_count", "lens", "start", "positions", "slots", "runs", "free_next",
+            "status")))
+        self._ref = ctypes.byref(self._c)
+
+
+def context_plan(plan: ContextPlan, add, release=None, commit: bool = False, stream=None) -> None:
+    """Plan a batch (``dg_context_plan``): request r adds ``add[r]`` tokens
+    (int32 CUDA tensor [B]).  ``release``: uint8 or bool CUDA tensor [B] of
+    requests that leave first.  ``commit``: the batch before becomes part of
+    the context; otherwise it is planned over."""
+    import torch
+    _need(add.dtype == torch.int32 and add.shape == (plan.B,) and add.is_contiguous() and add.device == plan.device,
+          "add must be a contiguous int32 tensor [B] on the plan's device")
+    _need(release is None or (release.dtype in (torch.uint8, torch.bool) and release.shape == (plan.B,) and
+                              release.is_contiguous() and release.device == plan.device),
+          "release must be a contiguous uint8 tensor [B] on the plan's device")
+    _call(plan.device, lib().dg_context_plan, "dg_context_plan", plan._ref, add.data_ptr(),
+          None if release is None else release.data_ptr(), 1 if commit else 0, _on(plan.device, stream))
+
+
+def context_status(plan: ContextPlan, stream=None) -> int:
+    """Synchronise and report (``dg_context_status``): 0, 10 (the last batch
+    was refused) or 9 (an append met a value that is not finite; cleared)."""
+    import torch
+    with torch.cuda.device(plan.device):
+        return int(lib().dg_context_status(plan._ref, _on(plan.device, stream)))
+
+
+class RopeFrequencies:
+    """Rotary frequencies on the device (``dg_rope_frequencies``): ``rot``
+    elements of each head turn; ``scaling`` "none", "linear", "ntk" or
+    "parts" by ``factor`` beyond ``original_length`` positions."""
+
+    def __init__(self, rot: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0,
+                 original_length: int = 4096, interleaved: bool = False, device=None):
+        import torch
+        _need(scaling in _ROPE_SCALING, f"scaling must be one of {sorted(_ROPE_SCALING)}")
+        f = np.zeros(max(int(rot), 2) // 2, np.float64)
+        mag = ctypes.c_float()
+        _check(lib().dg_rope_frequencies(rot, base, _ROPE_SCALING[scaling], factor, original_length,
+                                         f.ctypes.data_as(ctypes.c_void_p), ctypes.byref(mag)), "dg_rope_frequencies")
+        self.rot, self.interleaved, self.magnitude = int(rot), bool(interleaved), float(mag.value)
+        self.freq = torch.from_numpy(f).to("cuda" if device is None else device)
+        self._c = _RopeArgs(self.rot, int(self.interleaved), self.magnitude, self.freq.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+
+def rope(x, positions, frequencies: RopeFrequencies, out=None, stream=None):
+    """Rotary positions (``dg_rope``): bfloat16 ``x`` [rows, heads, dim], int32
+    ``positions`` [rows]; returns ``out`` (``x`` itself for in place)."""
+    import torch
+    if out is None:
+        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    _need(x.dim() == 3, "x must be [rows, heads, dim]")
+    rows, heads, dim = x.shape
+    _need(positions.dtype == torch.int32 and positions.dim() == 1 and positions.is_contiguous() and
+          positions.numel() >= rows and positions.device == x.device == frequencies.freq.device,
+          "positions must be a contiguous int32 tensor [rows] on x's device, and so the frequencies")
+    _need(out.shape == x.shape, "out must have x's shape")
+    if rows == 0:
+        return out
+    a, b = _heads(x, rows, heads, dim, x.device, "x"), _heads(out, rows, heads, dim, x.device, "out")
+    _call(x.device, lib().dg_rope, "dg_rope", ctypes.byref(a), ctypes.byref(b), rows, heads, dim,
+          positions.data_ptr(), frequencies._ref, _on(x.device, stream))
+    return out
+
+
+class ContextCache:
+    """One layer's cache (``dg_context_cache``): E4M3 codes ``k``, ``v`` (uint8
+    [pages, heads, 64, dim]) and power-of-two scales ``k_scale``, ``v_scale``
+    (float32 [pages, heads])."""
+
+    def __init__(self, pages: int, heads: int, dim: int, device=None):
+        import torch
+        device = "cuda" if device is None else device
+        _need(min(pages, heads, dim) >= 1, "ContextCache sizes must be positive")
+        self.pages, self.heads, self.dim = int(pages), int(heads), int(dim)
+        self.k = torch.zeros((pages, heads, PAGE, dim), dtype=torch.uint8, device=device)
+        self.v = torch.zeros_like(self.k)
+        self.k_scale = torch.ones((pages, heads), dtype=torch.float32, device=device)
+        self.v_scale = torch.ones_like(self.k_scale)
+        self.device = self.k.device
+        self._c = _Cache(self.pages, self.heads, self.dim, self.k.data_ptr(), self.v.data_ptr(),
+                         self.k_scale.data_ptr(), self.v_scale.data_ptr())
+        self._ref = ctypes.byref(self._c)
+
+
+def context_append(plan: ContextPlan, cache: ContextCache, k, v, rope: RopeFrequencies = None, stream=None) -> None:
+    """Write the batch's keys (rotated by their positions with ``rope``) and
+    values, bfloat16 [plan.rows, heads, dim], into their slots of ``cache``
+    (``dg_context_append``)."""
+    dev = plan.device
+    _need(cache.device == dev and (rope is None or rope.freq.device == dev),
+          "the cache and the frequencies must be on the plan's device")
+    a = _heads(k, plan.rows, cache.heads, cache.dim, dev, "k")
+    b = _heads(v, plan.rows, cache.heads, cache.dim, dev, "v")
+    _call(dev, lib().dg_context_append, "dg_context_append", plan._ref, cache._ref, ctypes.byref(a), ctypes.byref(b),
+          None if rope is None else rope._ref, _on(dev, stream))
+
+
+def context_workspace_size(rows: int, q_heads: int, kv_heads: int, dim: int) -> int:
+    """Bytes of workspace ``context_attention`` needs on the current device (0 if invalid)."""
+    return int(lib().dg_context_workspace_size(rows, q_heads, kv_heads, dim))
+
+
+class ContextWorkspace:
+    """Device scratch of ``context_attention`` for one shape (a zeroed torch
+    uint8 buffer; ``device_status`` reads its fault latch)."""
+
+    def __init__(self, rows: int, q_heads: int, kv_heads: int, dim: int, device=None, stream=None):
+        import torch
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        with torch.cuda.device(device):
+            n = context_workspace_size(rows, q_heads, kv_heads, dim)
+            if n == 0:
+                raise DGError(2, "context_workspace_size")
+            self.nbytes = n
+            self.buf = torch.empty(n, dtype=torch.uint8, device=device)
+            _check(lib().dg_workspace_init(_ptr(self.buf), ctypes.c_size_t(n), _stream(stream)), "dg_workspace_init")
+
+
+def context_attention(plan: ContextPlan, cache: ContextCache, q, out, ws: ContextWorkspace, causal=None,
+                      window: int = 0, scale: float = None, lse=None, max_new: int = 0, stream=None) -> None:
+    """Attention of the batch's rows over the cache (``dg_context_attention``):
+    bfloat16 ``q``, ``out`` [plan.rows, heads, dim]; ``causal`` uint8 or bool
+    CUDA tensor [B] (None: no request is causal); ``lse`` float32
+    [plan.rows, heads] or None; ``max_new`` the most rows of one request, if
+    known."""
+    import torch
+    dev = plan.device
+    _need(cache.device == dev and ws.buf.device == dev, "the cache and the workspace must be on the plan's device")
+    _need(q.dim() == 3, "q must be [rows, heads, dim]")
+    heads = q.shape[1]
+    a = _heads(q, plan.rows, heads, cache.dim, dev, "q")
+    b = _heads(out, plan.rows, heads, cache.dim, dev, "out")
+    _need(causal is None or (causal.dtype in (torch.uint8, torch.bool) and causal.shape == (plan.B,) and
+                             causal.is_contiguous() and causal.device == dev),
+          "causal must be a contiguous uint8 tensor [B] on the plan's device")
+    _need(lse is None or (lse.dtype == torch.float32 and lse.dim() == 2 and lse.shape[0] >= plan.rows and
+                          lse.shape[1] == heads and lse.is_contiguous() and lse.device == dev),
+          "lse must be a contiguous float32 tensor [rows, heads] on the plan's device")
+    _need(scale is None or scale > 0, "scale must be positive")
+    _call(dev, lib().dg_context_attention, "dg_context_attention", plan._ref, cache._ref, ctypes.byref(a),
+          ctypes.byref(b), heads, 0.0 if scale is None else scale, None if causal is None else causal.data_ptr(),
+          window, max_new, None if lse is None else lse.data_ptr(), ws.buf.data_ptr(), ws.nbytes, _on(dev, stream))
 
 
 def debug_gumbel(words, stream=None):

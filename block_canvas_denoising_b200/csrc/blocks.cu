@@ -8,9 +8,11 @@
 // far.  This file adds the noise canvas a block starts from (uniform over
 // the vocabulary, Figure 3) and the driver that chains the adaptive loop over
 // blocks, each block drawing its own random streams (the block index enters
-// the Philox counter's step word).
+// the Philox counter's step word).  With a context (context.cu) the driver
+// also plans every block's slots in it before the block's first step.
 #include <string.h>
 
+#include "context.h"
 #include "dg_device.cuh"
 #include "dg_internal.h"
 
@@ -71,12 +73,13 @@ extern "C" dg_status dg_init_canvas(const dg_shape* shape, const dg_params* para
   return DG_OK;
 }
 
-extern "C" dg_status dg_generate_blocks(const dg_shape* shape, const dg_params* params, const void* E,
-                                        const float* e_scale, int32_t n_blocks, dg_block_hidden_fn hidden_fn,
-                                        void* user, void* h_buf, int32_t* blocks, int32_t* steps_taken,
-                                        int32_t* canvas, int32_t* prev_argmax, uint8_t* accept, float* entropy,
-                                        int32_t* sampled, int32_t* argmax, int32_t* stop, void* workspace,
-                                        size_t ws_bytes, void* stream) {
+namespace {
+
+dg_status run_blocks(const dg_shape* shape, const dg_params* params, const void* E, const float* e_scale,
+                     int32_t n_blocks, dg_block_hidden_fn hidden_fn, void* user, const dg_context* ctx, int32_t* add,
+                     void* h_buf, int32_t* blocks, int32_t* steps_taken, int32_t* canvas, int32_t* prev_argmax,
+                     uint8_t* accept, float* entropy, int32_t* sampled, int32_t* argmax, int32_t* stop,
+                     void* workspace, size_t ws_bytes, void* stream) {
   dg_status st = check_shape_and_params(shape, params);
   if (st != DG_OK) return st;
   if (n_blocks < 1 || hidden_fn == nullptr || blocks == nullptr || steps_taken == nullptr || canvas == nullptr)
@@ -85,11 +88,29 @@ extern "C" dg_status dg_generate_blocks(const dg_shape* shape, const dg_params* 
   const int B = shape->B;
   const size_t rows = static_cast<size_t>(B) * shape->L;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (ctx != nullptr) {
+    if ((st = check_context(ctx)) != DG_OK) return st;
+    if (ctx->B != B || static_cast<size_t>(ctx->rows) < rows) return DG_ERR_UNSUPPORTED_SHAPE;
+    if (add == nullptr) return DG_ERR_INVALID_ARG;
+    if (device_sms() <= 0) return DG_ERR_NO_DEVICE;
+    // every request adds its canvas; the copy from host memory is staged by
+    // the runtime before the call returns
+    int32_t slots[DG_MAX_B];
+    for (int b = 0; b < B; ++b) slots[b] = shape->L;
+    if (!cuda_ok(cudaMemcpyAsync(add, slots, sizeof(int32_t) * B, cudaMemcpyHostToDevice, cs), "block lengths"))
+      return DG_ERR_CUDA;
+  }
   uint8_t has_prev[DG_MAX_B];
   for (int32_t j = 0; j < n_blocks; ++j) {
     dg_params pj = *params;
     pj.block = params->block + j;
     if ((st = dg_init_canvas(shape, &pj, canvas, stream)) != DG_OK) return st;
+    if (ctx != nullptr) {
+      // the block before (or the prompts) joins the context, this block's
+      // slots open behind it
+      if ((st = dg_context_plan(ctx, add, nullptr, 1, stream)) != DG_OK) return st;
+      if ((st = dg_context_status(ctx, stream)) != DG_OK) return st;
+    }
     memset(has_prev, 0, sizeof(has_prev));
     BlockCall call{hidden_fn, user, j, j > 0 ? blocks : nullptr};
     st = dg_denoise_loop(shape, &pj, E, e_scale, block_trampoline, &call, 0, h_buf, canvas, prev_argmax,
@@ -103,4 +124,29 @@ extern "C" dg_status dg_generate_blocks(const dg_shape* shape, const dg_params* 
   }
   if (cudaStreamSynchronize(cs) != cudaSuccess) return DG_ERR_CUDA;
   return DG_OK;
+}
+
+}  // namespace
+
+extern "C" dg_status dg_generate_blocks(const dg_shape* shape, const dg_params* params, const void* E,
+                                        const float* e_scale, int32_t n_blocks, dg_block_hidden_fn hidden_fn,
+                                        void* user, void* h_buf, int32_t* blocks, int32_t* steps_taken,
+                                        int32_t* canvas, int32_t* prev_argmax, uint8_t* accept, float* entropy,
+                                        int32_t* sampled, int32_t* argmax, int32_t* stop, void* workspace,
+                                        size_t ws_bytes, void* stream) {
+  return run_blocks(shape, params, E, e_scale, n_blocks, hidden_fn, user, nullptr, nullptr, h_buf, blocks,
+                    steps_taken, canvas, prev_argmax, accept, entropy, sampled, argmax, stop, workspace, ws_bytes,
+                    stream);
+}
+
+extern "C" dg_status dg_generate_blocks_context(const dg_shape* shape, const dg_params* params, const void* E,
+                                                const float* e_scale, int32_t n_blocks,
+                                                dg_block_hidden_fn hidden_fn, void* user, const dg_context* ctx,
+                                                int32_t* add, void* h_buf, int32_t* blocks, int32_t* steps_taken,
+                                                int32_t* canvas, int32_t* prev_argmax, uint8_t* accept,
+                                                float* entropy, int32_t* sampled, int32_t* argmax, int32_t* stop,
+                                                void* workspace, size_t ws_bytes, void* stream) {
+  if (ctx == nullptr) return DG_ERR_INVALID_ARG;
+  return run_blocks(shape, params, E, e_scale, n_blocks, hidden_fn, user, ctx, add, h_buf, blocks, steps_taken,
+                    canvas, prev_argmax, accept, entropy, sampled, argmax, stop, workspace, ws_bytes, stream);
 }

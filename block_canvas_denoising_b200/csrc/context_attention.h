@@ -1,0 +1,164 @@
+// context_attention.h -- what the attention kernels over the paged cache
+// share: their parameters, the split of a batch's work over the CTAs, and
+// the joining of the parts of a split item.
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "dg.h"
+#include "dg_device.cuh"
+
+namespace dg {
+
+struct AttnParams {
+  // the batch (dg_context)
+  const int32_t* table;
+  const int32_t* lens;
+  const int32_t* start;
+  int32_t B, max_pages, pages, rows;
+  // the cache
+  const float* k_scale;
+  const float* v_scale;
+  int32_t kv_heads, group;  // group = query heads per kv head
+  // queries and results
+  const uint8_t* q;
+  uint8_t* out;
+  int64_t q_row, q_head, out_row, out_head;  // strides in bytes
+  float* lse;
+  float scale_log2;  // logit factor times log2(e)
+  const uint8_t* causal;
+  int32_t window;
+  // workspace
+  float* part;        // [2 * grid][part_floats]
+  uint32_t* tickets;  // [grid], 0 between launches
+  uint32_t* err;
+  uint64_t wait_ns;
+  int32_t min_tiles;  // least tiles a CTA takes
+};
+
+// A request of the batch, as a kernel sees it: lengths a plan wrote, held
+// within what the tables and rows can address.
+struct Request {
+  int row0, nq, len;
+  bool causal;
+};
+DG_DEV Request request_of(const AttnParams& p, int r) {
+  Request q;
+  q.row0 = min(max(p.start[r], 0), p.rows);
+  q.nq = max(min(p.start[r + 1], p.rows) - q.row0, 0);
+  const int64_t room = static_cast<int64_t>(p.max_pages) * DG_PAGE;
+  q.len = static_cast<int>(min(static_cast<int64_t>(max(p.lens[r], 0)), room));
+  q.causal = p.causal != nullptr && p.causal[r] != 0;
+  return q;
+}
+
+// The keys [lo, hi] that query row i (of nq) of a request sees.
+DG_DEV int key_lo(const AttnParams& p, const Request& q, int i) {
+  return p.window > 0 ? max(q.len - q.nq + i - p.window + 1, 0) : 0;
+}
+DG_DEV int key_hi(const Request& q, int i) { return q.causal ? q.len - q.nq + i : q.len - 1; }
+
+// Work is cut into tiles: kM packed query rows (row rho is query row rho /
+// group, head rho % group of the kv head) by kKeys keys.  An item is one
+// (request, row tile, kv head) with all key tiles that some row of it sees
+// (one empty tile when none does, so that its zeros get written).  Items in
+// order, each with its key tiles in order, form one line of tiles; every CTA
+// takes an equal piece of that line (per = max(min_tiles, ceil(total /
+// grid)) tiles), whatever requests it spans: ragged batches and single long
+// contexts are split evenly by the same rule, and the rule follows the
+// lengths alone.
+template <int kM, int kKeys>
+struct Split {
+  static DG_DEV int row_tiles(const AttnParams& p, const Request& q) {
+    return static_cast<int>((static_cast<int64_t>(q.nq) * p.group + kM - 1) / kM);
+  }
+  static DG_DEV int item_tiles(const AttnParams& p, const Request& q, int mt, int* first) {
+    const int64_t rho = static_cast<int64_t>(mt) * kM;
+    const int i0 = static_cast<int>(rho / p.group);
+    const int i1 = min(static_cast<int>((rho + kM - 1) / p.group), q.nq - 1);
+    const int lo = key_lo(p, q, i0), hi = key_hi(q, i1);
+    *first = hi >= lo ? lo / kKeys : 0;
+    return hi >= lo ? hi / kKeys - lo / kKeys + 1 : 1;
+  }
+  // Fills before[0 .. B] (shared): tiles of the requests before r.  All
+  // threads of the block; ends with a barrier.
+  static DG_DEV void totals(const AttnParams& p, int64_t* before) {
+    for (int r = threadIdx.x; r < p.B; r += blockDim.x) {
+      const Request q = request_of(p, r);
+      const int mts = row_tiles(p, q);
+      int64_t n = 0;
+      int f;
+      if (!q.causal && p.window == 0) {
+        n = mts > 0 ? static_cast<int64_t>(mts) * item_tiles(p, q, 0, &f) : 0;
+      } else {
+        for (int m = 0; m < mts; ++m) n += item_tiles(p, q, m, &f);
+      }
+      before[r + 1] = n * p.kv_heads;
+    }
+    if (threadIdx.x == 0) before[0] = 0;
+    __syncthreads();
+    if (threadIdx.x < 32) {  // inclusive sums, 32 requests at a time
+      int64_t carry = 0;
+      for (int r0 = 0; r0 < p.B; r0 += 32) {
+        const int r = r0 + threadIdx.x;
+        int64_t v = r < p.B ? before[r + 1] : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
+          if (static_cast<int>(threadIdx.x) >= d) v += o;
+        }
+        v += carry;
+        if (r < p.B) before[r + 1] = v;
+        carry = __shfl_sync(0xffffffffu, v, 31);
+      }
+    }
+    __syncthreads();
+  }
+
+  int r, mt, h;          // the item
+  Request q;
+  int64_t begin;         // its first tile on the line
+  int tiles, first;      // its key tiles: first, first + 1, ...
+  // The item that holds tile `pos` of the line.
+  DG_DEV void find(const AttnParams& p, const int64_t* before, int64_t pos) {
+    int lo = 0, hi = p.B - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid + 1] > pos)
+        hi = mid;
+      else
+        lo = mid + 1;
+    }
+    r = lo;
+    q = request_of(p, r);
+    begin = before[r];
+    mt = 0;
+    while (true) {
+      tiles = item_tiles(p, q, mt, &first);
+      const int64_t all = static_cast<int64_t>(tiles) * p.kv_heads;
+      if (pos < begin + all) break;
+      begin += all;
+      ++mt;
+    }
+    h = static_cast<int>((pos - begin) / tiles);
+    begin += static_cast<int64_t>(h) * tiles;
+  }
+};
+
+// Join the softmax parts of one row of a split item: part i has its
+// reference m_i (log2), sum l_i and weighted values O_i, all relative to
+// 2^m_i.  Called with the parts in split order, so results do not depend on
+// which CTA came last.
+struct Joined {
+  float m = -FLT_MAX, l = 0.f;
+};
+DG_DEV float join_weight(float m, float top) { return exp2f(m - top); }
+
+DG_DEV float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+}  // namespace dg

@@ -18,13 +18,16 @@ constexpr size_t kAlign = 256;
 
 thread_local char t_last_error[256] = "";
 
-// Record a failed CUDA call's message for dg_last_error_message().
+}  // namespace
+
 bool cuda_ok(cudaError_t e, const char* what) {
   if (e == cudaSuccess) return true;
   snprintf(t_last_error, sizeof(t_last_error), "%s: %s (%d)", what, cudaGetErrorString(e),
            static_cast<int>(e));
   return false;
 }
+
+namespace {
 
 thread_local cudaEvent_t t_head_ev_start = nullptr;
 thread_local cudaEvent_t t_head_ev_stop = nullptr;
@@ -44,7 +47,8 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-// Current device's SM count, or -1 when it is not an sm_100 part.
+}  // namespace
+
 int device_sms() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return -1;
@@ -54,6 +58,8 @@ int device_sms() {
   if (major != 10) return -1;
   return sms;
 }
+
+namespace {
 
 dg_status check_shape(const dg_shape* s) {
   if (s == nullptr) return DG_ERR_INVALID_ARG;
@@ -94,8 +100,8 @@ float inv_tau_of(const dg_params& p, int k) {
   return static_cast<float>(1.0 / tau);
 }
 
-// 2-D tensor map over a row-major [rows, inner] matrix with elements of
-// `dtype` (`esize` bytes); box = box_inner x box_rows elements.
+}  // namespace
+
 bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t esize, CUtensorMapSwizzle swizzle,
                const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner, uint32_t box_rows) {
   auto fn = encode_fn();
@@ -108,6 +114,8 @@ bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t esize, CUte
                   swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
 }
+
+namespace {
 
 enum class StepMode { kFull, kHeadOnly, kMergeOnly };
 
@@ -484,6 +492,7 @@ const char* dg_error_string(dg_status s) {
     case DG_ERR_CALLBACK: return "hidden-state callback failed";
     case DG_ERR_NO_DEVICE: return "no sm_100 device";
     case DG_ERR_VALUE: return "input value outside the supported range";
+    case DG_ERR_CAPACITY: return "the context does not hold the batch";
   }
   return "unknown status";
 }

@@ -24,6 +24,7 @@ enum : uint32_t {
   kErrSelftest = 1u << 4,         // the bounded-wait self test ran out (expected)
   kErrHiddenRange = 1u << 5,      // FP8 head: a hidden-state value is not finite
   kErrProbRange = 1u << 6,        // self-conditioning: a probability block outside its encoding's range
+  kErrWaitContext = 1u << 7,      // context attention: gave up waiting for a copy or a matrix product
 };
 // Latched codes that report a value problem (DG_ERR_VALUE) rather than a
 // bounded wait that ran out (DG_ERR_TIMEOUT).
@@ -122,6 +123,19 @@ DG_DEV void tma_load_2d_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar,
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(cache_hint)
       : "memory");
 }
+
+// The same load for a CTA on its own.
+DG_DEV void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, uint64_t cache_hint) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4}], [%2], %5;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "l"(cache_hint)
+      : "memory");
+}
+
+// Order this thread's shared-memory accesses before later ones of the
+// asynchronous proxy (TMA, tcgen05 operands).
+DG_DEV void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 // ---------------------------------------------------------------------------
 // clusters

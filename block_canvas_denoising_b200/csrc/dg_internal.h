@@ -169,6 +169,14 @@ WsLayout ws_layout(const dg_shape& s, int max_pairs);
 
 // Text returned by dg_last_error_message() on this host thread.
 void set_last_error_message(const char* msg);
+// False, with the failed call's message recorded, unless e is cudaSuccess.
+bool cuda_ok(cudaError_t e, const char* what);
+// Current device's SM count, or -1 when it is not an sm_100 part.
+int device_sms();
+// 2-D tensor map over a row-major [rows, inner] matrix with elements of
+// `dtype` (`esize` bytes); box = box_inner x box_rows elements.
+bool encode_2d(CUtensorMap* map, CUtensorMapDataType dtype, uint32_t esize, CUtensorMapSwizzle swizzle,
+               const void* base, uint64_t inner, uint64_t rows, uint32_t box_inner, uint32_t box_rows);
 
 // The argument checks of dg_denoise_step other than those of the workspace
 // (shape, parameters, pointers, alignment, step range, device): DG_OK or

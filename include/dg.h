@@ -54,8 +54,10 @@ typedef enum {
   DG_ERR_TIMEOUT = 6,          /* a device-side bounded wait ran out */
   DG_ERR_CALLBACK = 7,         /* the hidden-state callback returned non-zero */
   DG_ERR_NO_DEVICE = 8,        /* no sm_100 device current */
-  DG_ERR_VALUE = 9             /* FP8 head: a hidden-state value is not finite
+  DG_ERR_VALUE = 9,            /* FP8 head: a hidden-state value is not finite
                                   (found on the device) */
+  DG_ERR_CAPACITY = 10         /* a context's pages, table or rows do not hold
+                                  the batch (found on the device) */
 } dg_status;
 
 typedef enum { DG_E_BF16 = 0, DG_E_FP8_E4M3 = 1 } dg_edtype;
@@ -368,6 +370,179 @@ dg_status dg_generate_blocks(const dg_shape* shape, const dg_params* params,
                              uint8_t* accept, float* entropy, int32_t* sampled,
                              int32_t* argmax, int32_t* stop,
                              void* workspace, size_t ws_bytes, void* stream);
+
+/* ---- the context of block-by-block generation ([Report] Figure 4) ---------
+ * dg_generate_blocks hands the committed blocks to the caller's model, which
+ * encodes them and appends them to the context that the next block's
+ * denoising steps attend to.  These entry points are that context: the block
+ * tables of a batch of requests, rotary positions, an 8-bit paged cache of
+ * keys and values, and the attention of new rows over it -- causal for
+ * encoding, bidirectional for a canvas, chosen per request ([Press]: the
+ * serving backends switch causal / bidirectional attention per request).
+ *
+ * A cache is a pool of pages of DG_PAGE token slots.  Token p of request r
+ * lives in slot p % DG_PAGE of page table[r][p / DG_PAGE].  A batch adds
+ * add[r] >= 0 tokens to every request; its token rows lie request after
+ * request in the batch's tensors, row start[r] + i being token held[r] + i.
+ * A batch is provisional: its tokens occupy slots behind the held ones, and
+ * may be written again (every denoising step of a canvas does), until a
+ * later plan commits them.  One dg_context serves all layers of a model;
+ * each layer has a dg_context_cache of its own. */
+#define DG_PAGE 64
+/* Entries of dg_context.runs for a batch of up to `rows` rows. */
+#define DG_CONTEXT_RUNS(rows, B) ((rows) / DG_PAGE + 2 * (B))
+
+typedef struct {
+  int32_t B;           /* requests, 1 .. DG_MAX_B */
+  int32_t rows;        /* token rows a batch may have */
+  int32_t pages;       /* pages of the pool */
+  int32_t max_pages;   /* pages one request may hold (row length of table) */
+  /* device state, owned by the caller */
+  int32_t* table;      /* [B][max_pages] page of each 64 tokens */
+  int32_t* held;       /* [B] committed tokens */
+  int32_t* free_list;  /* [pages] stack of free pages */
+  int32_t* free_count; /* [1] pages on the stack, provisional ones counted free */
+  /* device results of dg_context_plan for the provisional batch */
+  int32_t* lens;       /* [B] held + added tokens */
+  int32_t* start;      /* [B+1] first row of each request; start[B] = rows used */
+  int32_t* positions;  /* [rows] position of each row's token, -1 behind the last */
+  int64_t* slots;      /* [rows] page * DG_PAGE + slot of each row, -1 behind the last */
+  int32_t* runs;       /* [DG_CONTEXT_RUNS(rows, B)][4], 16-byte aligned: the pieces of
+                          the batch that lie in one page, (page, first row, first slot,
+                          tokens), in row order; (-1, 0, 0, 0) behind the last */
+  int32_t* free_next;  /* [1] free pages once the batch is committed */
+  int32_t* status;     /* [2] outcome of the last plan; latch of dg_context_append */
+} dg_context;
+
+/* dg_context_plan -- block tables and slot maps of a batch, from request
+ * lengths that may live on the device only.
+ *   add      int32 [B] device: tokens each request adds.
+ *   release  uint8 [B] device or NULL: requests that leave first; their held
+ *            pages go back on the stack (request after request, a request's
+ *            first page lowest) and the request starts empty.  Immediate: not
+ *            undone by a later plan.
+ *   commit   0: the previous batch is dropped and planned over; otherwise its
+ *            tokens become held ones (held = lens) first.
+ * New pages are popped from the top of the stack in request order.  A batch
+ * that does not fit is refused whole: it has no rows (start all 0), takes no
+ * page, and status[0] says why (see dg_context_status).  A new context has
+ * held, lens and status all 0, free_list = the pages and free_count =
+ * free_next = pages.  Asynchronous; one launch; may be captured. */
+dg_status dg_context_plan(const dg_context* ctx, const int32_t* add, const uint8_t* release, int32_t commit,
+                          void* stream);
+
+/* Synchronise `stream` and report the context: DG_ERR_CAPACITY when the last
+ * plan was refused (the reason in dg_last_error_message()), DG_ERR_VALUE when
+ * an append met a value that is not finite since the last call (the latch is
+ * cleared), else DG_OK. */
+dg_status dg_context_status(const dg_context* ctx, void* stream);
+
+/* A bf16 tensor [rows][heads][dim] on the device: dim contiguous, strides in
+ * elements and multiples of 8, data 16-byte aligned. */
+typedef struct {
+  void* data;
+  int64_t row_stride;
+  int64_t head_stride;
+} dg_heads;
+
+/* Rotary positions.  The pair j of a head, at position p, turns by the angle
+ * p * freq[j]:  (x, y) -> magnitude (x cos - y sin, x sin + y cos).  Pairs
+ * are elements (j, j + rot / 2), or (2j, 2j + 1) when interleaved, of the
+ * first `rot` elements; the rest of the head is left as it is. */
+typedef struct {
+  int32_t rot;         /* a multiple of 16, at most the head's dim */
+  int32_t interleaved;
+  float magnitude;
+  const double* freq;  /* [rot / 2] device, radians per position */
+} dg_rope_args;
+
+/* How frequencies are scaled for contexts longer than the model was trained
+ * on.  NONE: base^(-2j/rot).  LINEAR: those / factor.  NTK: base replaced by
+ * base * factor^(rot / (rot - 2)).  PARTS (Peng et al., YaRN, 2023): per
+ * frequency between the unscaled one (more than beta_fast = 32 turns in
+ * original_length positions) and the one / factor (less than beta_slow = 1),
+ * with magnitude 0.1 ln(factor) + 1. */
+typedef enum { DG_ROPE_NONE = 0, DG_ROPE_LINEAR = 1, DG_ROPE_NTK = 2, DG_ROPE_PARTS = 3 } dg_rope_scaling;
+
+/* Fill freq (HOST double [rot / 2]) and *magnitude (host).  base > 1,
+ * factor >= 1 (finite), original_length >= 1. */
+dg_status dg_rope_frequencies(int32_t rot, double base, int32_t scaling, double factor, int32_t original_length,
+                              double* freq, float* magnitude);
+
+/* out = x rotated: x, out bf16 [rows][heads][dim], dim 64 or 128; out may be
+ * x itself, and must not overlap it otherwise.  positions int32 [rows]
+ * (device): a row whose position is negative is left alone.  Angles are
+ * formed and reduced in float64, the rotation in float32, one rounding. */
+dg_status dg_rope(const dg_heads* x, const dg_heads* out, int32_t rows, int32_t heads, int32_t dim,
+                  const int32_t* positions, const dg_rope_args* rope, void* stream);
+
+/* One layer's cache.  Codes are E4M3, a value being code * scale of its
+ * (page, kv head); scales are powers of two. */
+typedef struct {
+  int32_t pages, heads, dim;   /* pages as in the context; 1 .. 1024 kv heads; dim 64 or 128 */
+  uint8_t* k;                  /* [pages][heads][DG_PAGE][dim], 16-byte aligned */
+  uint8_t* v;
+  float* k_scale;              /* [pages][heads] */
+  float* v_scale;
+} dg_context_cache;
+
+/* dg_context_append -- keys and values of the batch's rows into their slots.
+ *   k, v   bf16 [ctx->rows][heads][dim]; rows from start[B] on are not read.
+ *   rope   rotation of the keys by the rows' positions, or NULL.
+ * Each (page, head) of a run gets the least power of two s with
+ * max |x| <= 448 s over the run (at least 2^-100; 1 when all are 0), but not
+ * less than its old scale while it keeps tokens before the run; when it
+ * grows, the kept codes are rounded again.  Keys are rotated in float32 and
+ * rounded once, to nearest even.  A NaN is stored as 0 and an infinity as
+ * +-448 s with DG_ERR_VALUE latched (dg_context_status); neither counts
+ * towards s.  Slots behind the batch are left as they were. */
+dg_status dg_context_append(const dg_context* ctx, const dg_context_cache* cache, const dg_heads* k,
+                            const dg_heads* v, const dg_rope_args* rope, void* stream);
+
+/* Workspace of dg_context_attention on the current device (0 if invalid),
+ * zeroed once by dg_workspace_init(); its faults: dg_device_status(). */
+size_t dg_context_workspace_size(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t dim);
+
+/* dg_context_attention -- out = softmax(scale q . k) v of the batch's rows
+ * over their requests' tokens (held and added, read from the cache).
+ *   q, out   bf16 [ctx->rows][q_heads][dim]; query head i reads kv head
+ *            i / (q_heads / cache->heads).  out must not overlap q.
+ *   scale    factor of the logits, finite and >= 0; 0 stands for 1 / sqrt(dim).
+ *   causal   uint8 [B] device, or NULL: a request with a non-zero byte sees
+ *            tokens up to each row's own; the others (and NULL) see all
+ *            lens[r] tokens, behind the row too.
+ *   window   > 0: a row sees only tokens later than its own minus window
+ *            (its own counted: `window` tokens up to itself).  0: no limit.
+ *   max_new  the most rows one request of the batch has, when the host knows
+ *            it (0: not known): chooses the kernel, never the result's
+ *            meaning.
+ *   lse      float [rows][q_heads] or NULL: ln of the sum of exp(logits).
+ * A row that sees no token gives 0 (lse -inf).  A query that is not finite
+ * gives NaN in its own row and head only.  Cache codes must not be NaN
+ * (dg_context_append stores none); tokens on a page outside the pool are not
+ * seen.  Rows from start[B] on are left as they were.  Results do not depend
+ * on timing: splits and their joining follow the lengths alone.  Calls that
+ * share a workspace must not overlap. */
+dg_status dg_context_attention(const dg_context* ctx, const dg_context_cache* cache, const dg_heads* q,
+                               const dg_heads* out, int32_t q_heads, float scale, const uint8_t* causal,
+                               int32_t window, int32_t max_new, float* lse, void* workspace, size_t ws_bytes,
+                               void* stream);
+
+/* dg_generate_blocks with a context: before each block the library plans the
+ * block's B * 256 provisional rows (dg_context_plan with 256 added tokens per
+ * request, the batch before committed), so that hidden_fn finds the tables
+ * of its canvas in `ctx` and appends to and attends over its own layers'
+ * caches.  ctx->B = shape->B and ctx->rows >= B * 256; `add` is an int32 [B]
+ * device buffer that the call fills.  A batch planned before the call (the
+ * prompts) is committed by block 0's plan; the last block stays provisional.
+ * DG_ERR_CAPACITY when a block does not fit. */
+dg_status dg_generate_blocks_context(const dg_shape* shape, const dg_params* params, const void* E,
+                                     const float* e_scale, int32_t n_blocks, dg_block_hidden_fn hidden_fn,
+                                     void* user, const dg_context* ctx, int32_t* add, void* h_buf,
+                                     int32_t* blocks, int32_t* steps_taken, int32_t* canvas,
+                                     int32_t* prev_argmax, uint8_t* accept, float* entropy, int32_t* sampled,
+                                     int32_t* argmax, int32_t* stop, void* workspace, size_t ws_bytes,
+                                     void* stream);
 
 /* dg_denoise_step_noalloc -- dg_denoise_step for callers that cannot
  * allocate device memory for a workspace: a serving runtime that has carved

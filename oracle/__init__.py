@@ -17,6 +17,8 @@ Modules:
   blocks  -- block-by-block generation (encode & append) over the loop.
   selfcond -- the self-conditioning signal read as the expected embedding
              (its CUDA side is not built yet).
+  context -- the context of the blocks: block tables, rotary positions, the
+             append to the 8-bit paged cache, the attention over it.
 
 Parity pins: every function is checked in ``tests/test_oracle_*.py`` against
 something other than itself (closed forms, brute force in exact arithmetic,
@@ -24,11 +26,11 @@ independent library routines, invariants, chi-square).  The composed step has
 no worked example on the pages: its end-to-end values are pinned only through
 its parts.
 """
-from . import blocks, flog, loop, philox, replay, selfcond, step
+from . import blocks, context, flog, loop, philox, replay, selfcond, step
 from .blocks import generate_blocks
 from .loop import denoise_loop
 from .replay import replay_step
 from .step import Params, denoise_step
 
-__all__ = ["blocks", "flog", "loop", "philox", "replay", "selfcond", "step", "Params",
+__all__ = ["blocks", "context", "flog", "loop", "philox", "replay", "selfcond", "step", "Params",
            "denoise_step", "denoise_loop", "generate_blocks", "replay_step"]
