@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libdg.so")
 
 SOURCES = ["dg_api.cu", "head_sampler.cu", "hidden_split.cu", "merge_select.cu", "diagnostics.cu", "noalloc.cu",
            "selfcond.cu",
-           "blocks.cu", "loop_graph.cu", "context.cu", "context_attention.cu"]
+           "blocks.cu", "loop_graph.cu", "context.cu", "context_attention.cu",
+           "context_tiles.cu"]
 HEADERS = ["dg_device.cuh", "dg_internal.h", "per_device.h", "context.h", "context_attention.h"]
 
 

@@ -87,8 +87,6 @@ DG_DEV bool row_exponent(float top, int& e) {
   e = b == 0 ? 0 : min(14 - (b - 127), 120);
   return b < 255;
 }
-DG_DEV float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // -126 <= e <= 127
-
 // One warp walks its own pages with its own copies in flight and its own
 // softmax; the block's four warps meet once per item.  A page (64 keys) is 8
 // key tiles of mma.m16n8k16.  Which element of a head is "k index 2t" of an
@@ -482,16 +480,23 @@ int rows_grid() {
   return got ? n : -1;
 }
 
-// Workspace: the fault latch, the tickets, the parts.
+// Workspace: the fault latch, the tickets, the parts.  Sized for both
+// kernels, so that one workspace serves every batch of a shape.
 struct AttnWs {
+  int rows_grid, tiles_grid;
   size_t tickets, part, total;
 };
-AttnWs attn_ws(int grid, size_t part_floats) {
-  AttnWs w;
-  w.tickets = kWsAlign;
-  w.part = w.tickets + (static_cast<size_t>(grid) * 4 + kWsAlign - 1) / kWsAlign * kWsAlign;
-  w.total = w.part + static_cast<size_t>(grid) * 2 * part_floats * 4;
-  return w;
+bool attn_ws(int dim, AttnWs* w) {
+  w->rows_grid = dim == 128 ? rows_grid<128>() : rows_grid<64>();
+  w->tiles_grid = tiles_grid(dim);
+  if (w->rows_grid < 1 || w->tiles_grid < 1) return false;
+  const size_t rows_floats = dim == 128 ? RowsCfg<128>::kPartFloats : RowsCfg<64>::kPartFloats;
+  const size_t a = static_cast<size_t>(w->rows_grid) * rows_floats, b = w->tiles_grid * tiles_part_floats(dim);
+  const int grid = w->rows_grid > w->tiles_grid ? w->rows_grid : w->tiles_grid;
+  w->tickets = kWsAlign;
+  w->part = w->tickets + (static_cast<size_t>(grid) * 4 + kWsAlign - 1) / kWsAlign * kWsAlign;
+  w->total = w->part + 2 * sizeof(float) * (a > b ? a : b);
+  return true;
 }
 
 bool shape_ok(int64_t rows, int64_t q_heads, int64_t kv_heads, int dim) {
@@ -511,9 +516,8 @@ extern "C" {
 size_t dg_context_workspace_size(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t dim) {
   if (!shape_ok(rows, q_heads, kv_heads, dim)) return 0;
   if (device_sms() <= 0) return 0;
-  const int grid = dim == 128 ? rows_grid<128>() : rows_grid<64>();
-  if (grid < 1) return 0;
-  return attn_ws(grid, dim == 128 ? RowsCfg<128>::kPartFloats : RowsCfg<64>::kPartFloats).total;
+  AttnWs ws;
+  return attn_ws(dim, &ws) ? ws.total : 0;
 }
 
 dg_status dg_context_attention(const dg_context* ctx, const dg_context_cache* cache, const dg_heads* q,
@@ -531,9 +535,11 @@ dg_status dg_context_attention(const dg_context* ctx, const dg_context_cache* ca
   if (device_sms() <= 0) return DG_ERR_NO_DEVICE;
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & (kWsAlign - 1)) != 0) return DG_ERR_INVALID_ARG;
   const int dim = cache->dim;
-  const int grid = dim == 128 ? rows_grid<128>() : rows_grid<64>();
-  if (grid < 1) return DG_ERR_CUDA;
-  const AttnWs ws = attn_ws(grid, dim == 128 ? RowsCfg<128>::kPartFloats : RowsCfg<64>::kPartFloats);
+  AttnWs ws;
+  if (!attn_ws(dim, &ws)) {
+    set_last_error_message("no CTA of a context attention kernel fits on this device");
+    return DG_ERR_CUDA;
+  }
   if (ws_bytes < ws.total) return DG_ERR_WORKSPACE;
 
   AttnParams p;
@@ -565,7 +571,6 @@ dg_status dg_context_attention(const dg_context* ctx, const dg_context_cache* ca
   p.tickets = reinterpret_cast<uint32_t*>(wsb + ws.tickets);
   p.part = reinterpret_cast<float*>(wsb + ws.part);
   p.wait_ns = kDefaultWaitNs;
-  p.min_tiles = kRowsWarps;
 
   CUtensorMap tmK, tmV;
   const uint64_t crows = static_cast<uint64_t>(cache->pages) * cache->heads * DG_PAGE;
@@ -576,10 +581,19 @@ dg_status dg_context_attention(const dg_context* ctx, const dg_context_cache* ca
     return DG_ERR_CUDA;
   }
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  // One row tile of the rows kernel is 16 rows; the tiles kernel works on 256
+  // whether they are there or not.
+  const int64_t most = static_cast<int64_t>(max_new > 0 && max_new < ctx->rows ? max_new : ctx->rows) * p.group;
+  if (most > kRowsM) {
+    p.min_tiles = 1;
+    return cuda_ok(launch_attention_tiles(dim, tmK, tmV, p, ws.tiles_grid, cs), "context attention launch") ? DG_OK
+                                                                                                       : DG_ERR_CUDA;
+  }
+  p.min_tiles = kRowsWarps;
   if (dim == 128)
-    attention_rows_kernel<128><<<grid, kRowsThreads, RowsCfg<128>::kSmem, cs>>>(tmK, tmV, p);
+    attention_rows_kernel<128><<<ws.rows_grid, kRowsThreads, RowsCfg<128>::kSmem, cs>>>(tmK, tmV, p);
   else
-    attention_rows_kernel<64><<<grid, kRowsThreads, RowsCfg<64>::kSmem, cs>>>(tmK, tmV, p);
+    attention_rows_kernel<64><<<ws.rows_grid, kRowsThreads, RowsCfg<64>::kSmem, cs>>>(tmK, tmV, p);
   return cuda_ok(cudaGetLastError(), "context attention launch") ? DG_OK : DG_ERR_CUDA;
 }
 

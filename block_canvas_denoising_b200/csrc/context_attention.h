@@ -53,6 +53,8 @@ DG_DEV Request request_of(const AttnParams& p, int r) {
   return q;
 }
 
+DG_DEV float pow2i(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // -126 <= e <= 127
+
 // The keys [lo, hi] that query row i (of nq) of a request sees.
 DG_DEV int key_lo(const AttnParams& p, const Request& q, int i) {
   return p.window > 0 ? max(q.len - q.nq + i - p.window + 1, 0) : 0;
@@ -81,8 +83,19 @@ struct Split {
     *first = hi >= lo ? lo / kKeys : 0;
     return hi >= lo ? hi / kKeys - lo / kKeys + 1 : 1;
   }
+  // Sum over lanes of the tiles of row tiles mt0 + lane, mt0 + 32 + lane, ...
+  static DG_DEV int64_t warp_tiles(const AttnParams& p, const Request& q, int mts) {
+    int64_t n = 0;
+    int f;
+    for (int m = static_cast<int>(threadIdx.x & 31); m < mts; m += 32) n += item_tiles(p, q, m, &f);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) n += __shfl_xor_sync(0xffffffffu, n, d);
+    return n;
+  }
   // Fills before[0 .. B] (shared): tiles of the requests before r.  All
-  // threads of the block; ends with a barrier.
+  // threads of the block; ends with a barrier.  A thread per request; the
+  // requests whose row tiles differ in length (causal, window) and are many
+  // get a warp each.
   static DG_DEV void totals(const AttnParams& p, int64_t* before) {
     for (int r = threadIdx.x; r < p.B; r += blockDim.x) {
       const Request q = request_of(p, r);
@@ -91,12 +104,21 @@ struct Split {
       int f;
       if (!q.causal && p.window == 0) {
         n = mts > 0 ? static_cast<int64_t>(mts) * item_tiles(p, q, 0, &f) : 0;
-      } else {
+      } else if (mts <= 8) {
         for (int m = 0; m < mts; ++m) n += item_tiles(p, q, m, &f);
+      } else {
+        n = -1;
       }
-      before[r + 1] = n * p.kv_heads;
+      before[r + 1] = n < 0 ? n : n * p.kv_heads;
     }
     if (threadIdx.x == 0) before[0] = 0;
+    __syncthreads();
+    for (int r = threadIdx.x >> 5; r < p.B; r += blockDim.x >> 5) {
+      if (before[r + 1] >= 0) continue;  // the same for the whole warp
+      const Request q = request_of(p, r);
+      const int64_t n = warp_tiles(p, q, row_tiles(p, q));
+      if ((threadIdx.x & 31) == 0) before[r + 1] = n * p.kv_heads;
+    }
     __syncthreads();
     if (threadIdx.x < 32) {  // inclusive sums, 32 requests at a time
       int64_t carry = 0;
@@ -120,7 +142,8 @@ struct Split {
   Request q;
   int64_t begin;         // its first tile on the line
   int tiles, first;      // its key tiles: first, first + 1, ...
-  // The item that holds tile `pos` of the line.
+  // The item that holds tile `pos` of the line.  All lanes of a warp, with
+  // the same arguments.
   DG_DEV void find(const AttnParams& p, const int64_t* before, int64_t pos) {
     int lo = 0, hi = p.B - 1;
     while (lo < hi) {
@@ -133,26 +156,44 @@ struct Split {
     r = lo;
     q = request_of(p, r);
     begin = before[r];
-    mt = 0;
-    while (true) {
-      tiles = item_tiles(p, q, mt, &first);
-      const int64_t all = static_cast<int64_t>(tiles) * p.kv_heads;
-      if (pos < begin + all) break;
-      begin += all;
-      ++mt;
+    if (!q.causal && p.window == 0) {  // every row tile sees the same keys
+      tiles = item_tiles(p, q, 0, &first);
+      const int64_t n = (pos - begin) / tiles;
+      mt = static_cast<int>(n / p.kv_heads);
+      h = static_cast<int>(n % p.kv_heads);
+      begin += n * tiles;
+      return;
     }
-    h = static_cast<int>((pos - begin) / tiles);
-    begin += static_cast<int64_t>(h) * tiles;
+    const int lane = static_cast<int>(threadIdx.x & 31);
+    const int mts = row_tiles(p, q);
+    for (int m0 = 0;; m0 += 32) {  // 32 row tiles at a time
+      int f = 0;
+      const int n = m0 + lane < mts ? item_tiles(p, q, m0 + lane, &f) : 0;
+      int64_t upto = static_cast<int64_t>(n) * p.kv_heads;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int64_t o = __shfl_up_sync(0xffffffffu, upto, d);
+        if (lane >= d) upto += o;
+      }
+      const unsigned behind = __ballot_sync(0xffffffffu, begin + upto > pos);
+      if (behind == 0 && m0 + 32 < mts) {
+        begin += __shfl_sync(0xffffffffu, upto, 31);
+        continue;
+      }
+      const int at = behind == 0 ? 31 : __ffs(behind) - 1;
+      tiles = __shfl_sync(0xffffffffu, n, at);
+      first = __shfl_sync(0xffffffffu, f, at);
+      begin += __shfl_sync(0xffffffffu, upto, at) - static_cast<int64_t>(tiles) * p.kv_heads;
+      mt = m0 + at;
+      h = static_cast<int>((pos - begin) / tiles);
+      begin += static_cast<int64_t>(h) * tiles;
+      return;
+    }
   }
 };
 
-// Join the softmax parts of one row of a split item: part i has its
-// reference m_i (log2), sum l_i and weighted values O_i, all relative to
-// 2^m_i.  Called with the parts in split order, so results do not depend on
-// which CTA came last.
-struct Joined {
-  float m = -FLT_MAX, l = 0.f;
-};
+// The weight of a part whose logits are relative to 2^m when parts are joined
+// relative to 2^top.
 DG_DEV float join_weight(float m, float top) { return exp2f(m - top); }
 
 DG_DEV float exp2_fast(float x) {
@@ -160,5 +201,12 @@ DG_DEV float exp2_fast(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+
+// The kernel for many rows (context_tiles.cu): its resident CTAs on the
+// current device (-1: none), the floats of one part, its launch.
+int tiles_grid(int dim);
+size_t tiles_part_floats(int dim);
+cudaError_t launch_attention_tiles(int dim, const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& p,
+                                   int grid, cudaStream_t stream);
 
 }  // namespace dg

@@ -1,0 +1,858 @@
+// context_tiles.cu -- attention over the 8-bit paged cache for many rows per
+// kv head (canvases, prompts), on the 5th-generation tensor cores.
+//
+// A CTA works on 256 packed query rows (two groups of 128) by 128 keys (two
+// pages).  Per tile and group:
+//   S = Q K^T   tcgen05.mma kind::f8f6f4, K's codes as the cache holds them
+//               and Q as two E4M3 terms q = (q1 + q2) 2^-e per row, which
+//               is exact for every element down to 2^-9 of the row's largest
+//               (below that, off by at most 2^-17 of it); two terms at the
+//               E4M3 rate cost what one bf16 product would, without a copy
+//               of K in 16 bits;
+//   P           one thread per row: running maximum, weights 2^(x + e - m +
+//               kWeightLog2) in float16 written over S in tensor memory;
+//   O += P V    tcgen05.mma kind::f16 with P from tensor memory and V's codes
+//               widened to float16 (exact) by four warps of their own.
+// The running maximum only moves when it is exceeded by more than 2^8, so
+// O is seldom rescaled; weights stay below 2^(kWeightLog2 + 8) = 2^14.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+
+#include "context_attention.h"
+#include "dg_internal.h"
+#include "per_device.h"
+
+namespace dg {
+
+namespace {
+
+constexpr int kGroupRows = 128;
+constexpr int kTilesM = 2 * kGroupRows;
+constexpr int kTilesN = 2 * DG_PAGE;  // keys per tile
+constexpr float kWeightLog2 = 6.f;
+constexpr float kLazyLog2 = 8.f;      // the maximum may be exceeded by 2^8 before it moves
+
+// Warp roles.  Tensor memory is read by lane quarter (warp % 4), so each
+// softmax group is four consecutive warps; the issuing thread sits in the
+// lowest warp, which the schedulers favour.
+constexpr int kMmaWarp1 = 0, kLoadWarp = 1, kPlanWarp = 2;  // warp 3 is idle
+constexpr int kSoftWarp0 = 4, kConvWarp0 = 12;
+constexpr int kTilesThreads = 512;
+// Registers: 512 threads x 128 at launch; the softmax warps hold a row of S.
+constexpr int kSoftRegs = 192, kOtherRegs = 64;
+static_assert(256 * kSoftRegs + 256 * kOtherRegs <= 512 * 128, "register split exceeds the launch's");
+
+constexpr int kScaleSlots = 8;  // tiles whose page scales are kept
+constexpr int kPieceSlots = 8;  // pieces of work known ahead; the groups are at most kKStages tiles apart
+
+template <int kDim>
+struct TilesCfg {
+  static constexpr int kRow = kDim;                             // bytes of a row of codes
+  static constexpr int kQBytes = kGroupRows * kRow;             // one term of one group
+  static constexpr int kKBytes = kTilesN * kRow;
+  static constexpr int kVhBytes = kTilesN * kDim * 2;
+  static constexpr int kKStages = kDim == 128 ? 3 : 4, kV8Stages = kDim == 128 ? 2 : 4, kVhStages = 2;
+  static constexpr int kOffK = 4 * kQBytes;
+  static constexpr int kOffV8 = kOffK + kKStages * kKBytes;
+  static constexpr int kOffVh = kOffV8 + kV8Stages * kKBytes;
+  static constexpr int kSmem = kOffVh + kVhStages * kVhBytes + 1024;
+  static constexpr int kPartFloats = kTilesM * (kDim + 2);
+  static_assert(kKStages < kPieceSlots && kKStages < kScaleSlots - 1, "slots are written before they are read");
+  static_assert(kSmem <= 220 * 1024, "attention tiles exceed the shared memory of an SM");
+};
+
+// One piece of a CTA's work: some key tiles of one item.
+struct Piece {
+  int r, row0, nq, len, causal, mt, h;
+  int tile0, tiles;     // key tiles
+  int groups;           // 1 or 2 groups have rows
+  int whole, c0, parts; // the whole item, or the split it belongs to
+  int last;             // no piece: the end
+};
+
+struct TilesShared {
+  int64_t before[DG_MAX_B + 1];
+  Piece piece[kPieceSlots];
+  float4 scale[kScaleSlots];  // (k scale, value exponent) of the tile's two pages; k scale < 0: page not there
+  uint64_t k_full[4], k_empty[4], v8_full[4], v8_empty[4], vh_full[2], vh_empty[2];
+  uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
+  uint64_t parts_written, last_known;
+  uint64_t sc_full[kScaleSlots], piece_full[kPieceSlots], piece_empty[kPieceSlots];
+  uint32_t tmem;
+  uint32_t last_part;
+};
+
+// ---- tcgen05 for a CTA on its own -----------------------------------------
+DG_DEV void tmem_alloc1(uint32_t dst, uint32_t cols) {
+  asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst), "r"(cols) : "memory");
+}
+DG_DEV void tmem_relinquish1() { asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory"); }
+DG_DEV void tmem_dealloc1(uint32_t addr, uint32_t cols) {
+  asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr), "r"(cols) : "memory");
+}
+DG_DEV void tc_commit1(uint32_t bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+// D[tmem] (+)= A[smem] B[smem]^T, E4M3, both K-major (K = 32).
+DG_DEV void mma_e4m3_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] B[smem], float16 (K = 16).
+DG_DEV void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// 32 consecutive 32-bit columns of this thread's tensor-memory lane.
+DG_DEV void tmem_ld32(uint32_t addr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+// Wait for this thread's loads; the registers pass through, so that nothing
+// that uses them moves ahead of the wait.
+DG_DEV void tmem_ld_wait(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+DG_DEV void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+DG_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+DG_DEV bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+
+// Descriptor of a K-major tile whose rows are one swizzle span (128 or 64
+// bytes), 8-row groups one after another.
+template <int kRow>
+DG_DEV uint64_t desc_k_major(uint32_t saddr) {
+  uint64_t d = (saddr & 0x3FFFFu) >> 4;
+  d |= static_cast<uint64_t>(1u) << 16;
+  d |= static_cast<uint64_t>((8 * kRow) >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(kRow == 128 ? 2u : 4u) << 61;
+  return d;
+}
+// Descriptor of an MN-major float16 tile in the 128-byte swizzle: rows are
+// keys (K), 64 elements of the head (N) each; 8-key groups 1024 bytes apart
+// (stride), the next 64 elements kTilesN rows further (leading).
+DG_DEV uint64_t desc_mn_major(uint32_t saddr) {
+  uint64_t d = (saddr & 0x3FFFFu) >> 4;
+  d |= static_cast<uint64_t>((kTilesN * 128) >> 4) << 16;
+  d |= static_cast<uint64_t>(1024u >> 4) << 32;
+  d |= static_cast<uint64_t>(1u) << 46;
+  d |= static_cast<uint64_t>(2u) << 61;
+  return d;
+}
+// kind::f16, A and B float16 (format 0), f32 accumulator, B MN-major (bit 16).
+__host__ __device__ constexpr uint32_t idesc_f16_bmn(int M, int N) {
+  return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+DG_DEV uint32_t f2_to_e4m3x2(float lo, float hi) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+}
+DG_DEV uint32_t e4m3x2_to_half2(uint32_t w) {  // low 16 bits
+  uint32_t d;
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(d) : "r"(w));
+  return d;
+}
+DG_DEV uint32_t pack_half2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// A row's place in the batch.
+struct Row {
+  bool live;
+  int lo, hi;            // keys it sees
+  int64_t token, head;   // row of the batch, query head
+};
+DG_DEV Row row_of(const AttnParams& p, const Piece& w, int row) {
+  const int64_t rho = static_cast<int64_t>(w.mt) * kTilesM + row;
+  const int i = static_cast<int>(rho / p.group);
+  Row o;
+  o.live = i < w.nq;
+  o.token = w.row0 + i;
+  o.head = static_cast<int64_t>(w.h) * p.group + rho % p.group;
+  Request q;
+  q.nq = w.nq;
+  q.len = w.len;
+  q.causal = w.causal != 0;
+  o.lo = o.live ? key_lo(p, q, i) : 1;
+  o.hi = o.live ? key_hi(q, i) : 0;
+  return o;
+}
+
+// This thread's query row as two E4M3 terms into shared memory (K-major,
+// swizzled); returns the factor that turns a dot product of the terms into a
+// logit in units of log2.
+template <int kDim>
+DG_DEV float prepare_q(const AttnParams& p, const Row& o, uint8_t* q1, uint8_t* q2, int row) {
+  uint4 w[kDim / 8];
+  const uint8_t* src = p.q + o.token * p.q_row + o.head * p.q_head;
+#pragma unroll
+  for (int c = 0; c < kDim / 8; ++c) w[c] = o.live ? *reinterpret_cast<const uint4*>(src + 16 * c) : make_uint4(0, 0, 0, 0);
+  // the largest magnitude, as an integer maximum over the bf16 halves
+  uint32_t top = 0;
+#pragma unroll
+  for (int c = 0; c < kDim / 8; ++c) {
+    const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) top = max(max(top, (u[j] << 16) & 0x7FFFFFFFu), u[j] & 0x7FFF0000u);
+  }
+  const int b = static_cast<int>(top >> 23);
+  const int e = b == 0 ? 0 : min(7 - (b - 127), 120);  // largest magnitude to [2^7, 2^8)
+  const bool finite = b < 255;
+  const float f = pow2i(e);
+#pragma unroll
+  for (int c = 0; c < kDim / 16; ++c) {
+    uint32_t t1[4], t2[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint4 v = w[2 * c + (j >> 1)];
+      const uint32_t a = (j & 1) ? v.z : v.x, d = (j & 1) ? v.w : v.y;
+      const float x[4] = {__uint_as_float(a << 16) * f, __uint_as_float(a & 0xFFFF0000u) * f,
+                          __uint_as_float(d << 16) * f, __uint_as_float(d & 0xFFFF0000u) * f};
+      const uint32_t lo = f2_to_e4m3x2(x[0], x[1]), hi = f2_to_e4m3x2(x[2], x[3]);
+      const uint32_t hl = e4m3x2_to_half2(lo), hh = e4m3x2_to_half2(hi);
+      const float2 bl = __half22float2(*reinterpret_cast<const __half2*>(&hl));
+      const float2 bh = __half22float2(*reinterpret_cast<const __half2*>(&hh));
+      t1[j] = finite ? (lo | hi << 16) : 0x7F7F7F7Fu;  // a row that is not finite: NaN throughout
+      t2[j] = f2_to_e4m3x2(x[0] - bl.x, x[1] - bl.y) | f2_to_e4m3x2(x[2] - bh.x, x[3] - bh.y) << 16;
+    }
+    const int at = kDim == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+    *reinterpret_cast<uint4*>(q1 + at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+    *reinterpret_cast<uint4*>(q2 + at) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+  }
+  return finite ? p.scale_log2 * pow2i(-e) : 1.f;
+}
+
+template <int kDim>
+__global__ void __launch_bounds__(kTilesThreads, 1)
+attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                       const __grid_constant__ AttnParams p) {
+  using Cfg = TilesCfg<kDim>;
+  using S = Split<kTilesM, kTilesN>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ TilesShared sh;
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < 4; ++s) {
+      mbar_init(smem_u32(&sh.k_full[s]), 1);
+      mbar_init(smem_u32(&sh.k_empty[s]), 2);
+      mbar_init(smem_u32(&sh.v8_full[s]), 1);
+      mbar_init(smem_u32(&sh.v8_empty[s]), 4);
+    }
+    for (int s = 0; s < kPieceSlots; ++s) {
+      mbar_init(smem_u32(&sh.piece_full[s]), 1);
+      mbar_init(smem_u32(&sh.piece_empty[s]), 14);  // issuer, loader, 4 converter and 8 softmax warps
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(smem_u32(&sh.vh_full[s]), 4);
+      mbar_init(smem_u32(&sh.vh_empty[s]), 2);
+      mbar_init(smem_u32(&sh.q_full[s]), 4);
+      mbar_init(smem_u32(&sh.s_full[s]), 1);
+      mbar_init(smem_u32(&sh.p_full[s]), 4);
+      mbar_init(smem_u32(&sh.o_done[s]), 1);
+    }
+    for (int s = 0; s < kScaleSlots; ++s) mbar_init(smem_u32(&sh.sc_full[s]), 1);
+    mbar_init(smem_u32(&sh.parts_written), 8);
+    mbar_init(smem_u32(&sh.last_known), 1);
+    fence_mbarrier_init();
+  }
+  if (warp == kMmaWarp1) {
+    tmem_alloc1(smem_u32(&sh.tmem), 512);
+    tmem_relinquish1();
+  }
+  S::totals(p, sh.before);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sh.tmem;
+  // columns: S (and P over it) of group g at 128 g, O at 256 + 128 g
+  const int64_t total = sh.before[p.B];
+  const int64_t even = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t per = even > p.min_tiles ? even : p.min_tiles;
+
+  bool ok = true;
+  auto wait = [&](uint64_t& bar, uint32_t parity) {
+    if (ok && !mbar_wait_bounded(smem_u32(&bar), parity, p.wait_ns)) {
+      ok = false;
+      atomicOr(p.err, kErrWaitContext);
+    }
+  };
+  // the piece list, read by every role at its own pace
+  auto next_piece = [&](int n) -> const Piece& {
+    wait(sh.piece_full[n % kPieceSlots], (n / kPieceSlots) & 1);
+    return sh.piece[n % kPieceSlots];
+  };
+  auto done_piece = [&](int n) {  // one lane per warp
+    mbar_arrive(smem_u32(&sh.piece_empty[n % kPieceSlots]));
+  };
+
+  // A warpgroup's four warps change their registers together, so the roles
+  // are told apart by warpgroup first.
+  if (warp < kSoftWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+  if (warp == kPlanWarp) {
+    // ---- the pieces of this CTA's range, some ahead of their use
+    int64_t pos = blockIdx.x * per;
+    const int64_t end = min(pos + per, total);
+    for (int n = 0; ok; ++n) {
+      if (n >= kPieceSlots) wait(sh.piece_empty[n % kPieceSlots], ((n / kPieceSlots) & 1) ^ 1);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      Piece w;
+      w.last = pos >= end;
+      if (!w.last) {
+        S it;
+        it.find(p, sh.before, pos);
+        const int64_t item_end = it.begin + it.tiles;
+        w.r = it.r;
+        w.row0 = it.q.row0;
+        w.nq = it.q.nq;
+        w.len = it.q.len;
+        w.causal = it.q.causal;
+        w.mt = it.mt;
+        w.h = it.h;
+        w.tile0 = it.first + static_cast<int>(pos - it.begin);
+        w.tiles = static_cast<int>(min(item_end, end) - pos);
+        w.groups = static_cast<int64_t>(it.q.nq) * p.group - static_cast<int64_t>(it.mt) * kTilesM > kGroupRows ? 2 : 1;
+        w.whole = w.tiles == it.tiles;
+        w.c0 = static_cast<int>(it.begin / per);
+        w.parts = static_cast<int>((item_end - 1) / per) - w.c0 + 1;
+        pos += w.tiles;
+      }
+      if (lane == 0) {
+        sh.piece[n % kPieceSlots] = w;
+        mbar_arrive(smem_u32(&sh.piece_full[n % kPieceSlots]));
+      }
+      if (w.last) break;
+    }
+  } else if (warp == kLoadWarp) {
+    // ---- copies of K and V codes, and the pages' scales
+    const uint64_t policy = policy_evict_last();  // row tiles of a head share its keys
+    int T = 0, issued_k = 0, issued_v = 0;
+    for (int n = 0; ok; ++n) {
+      const Piece& w = next_piece(n);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok || w.last) break;
+      const int page0 = 2 * w.tile0, pages = 2 * w.tiles;
+      const int last_page = (w.len + DG_PAGE - 1) / DG_PAGE - 1;
+      int id = 0;
+      float ks = 0.f, ve = 0.f;
+      for (int j = 0; j < w.tiles && ok; ++j, ++T) {
+        if ((j & 15) == 0) {  // ids and scales of the next 32 pages, one per lane
+          const int m = 2 * j + lane, pg = page0 + m;
+          id = -1;
+          if (m < pages && pg <= last_page && pg < p.max_pages) id = p.table[static_cast<size_t>(w.r) * p.max_pages + pg];
+          if (id < 0 || id >= p.pages) {
+            id = p.pages;  // outside the tensor: the copy fills zeros
+            ks = -1.f;     // and its keys are not seen
+            ve = 0.f;
+          } else {
+            const size_t at = static_cast<size_t>(id) * p.kv_heads + w.h;
+            ks = p.k_scale[at];
+            ve = static_cast<float>(static_cast<int>(__float_as_uint(p.v_scale[at]) >> 23) - 127);
+          }
+        }
+        const int a = (2 * j) & 31;
+        const int id0 = __shfl_sync(0xffffffffu, id, a), id1 = __shfl_sync(0xffffffffu, id, a + 1);
+        const float ks0 = __shfl_sync(0xffffffffu, ks, a), ks1 = __shfl_sync(0xffffffffu, ks, a + 1);
+        const float ve0 = __shfl_sync(0xffffffffu, ve, a), ve1 = __shfl_sync(0xffffffffu, ve, a + 1);
+        const int y0 = (id0 * p.kv_heads + w.h) * DG_PAGE, y1 = (id1 * p.kv_heads + w.h) * DG_PAGE;
+        const int st = T % Cfg::kKStages, sv = T % Cfg::kV8Stages;
+        wait(sh.k_empty[st], ((T / Cfg::kKStages) & 1) ^ 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          // slot T % 8 was last read for tile T - 8; with K stage T % kKStages
+          // free, every softmax warp is past tile T - kKStages - 1
+          sh.scale[T % kScaleSlots] = make_float4(ks0, ve0, ks1, ve1);
+          mbar_arrive(smem_u32(&sh.sc_full[T % kScaleSlots]));
+          const uint32_t bar = smem_u32(&sh.k_full[st]);
+          const uint32_t dst = smem_u32(smem + Cfg::kOffK + st * Cfg::kKBytes);
+          mbar_arrive_expect_tx(bar, Cfg::kKBytes);
+          tma_load_2d(dst, &tmK, bar, 0, y0, policy);
+          tma_load_2d(dst + Cfg::kKBytes / 2, &tmK, bar, 0, y1, policy);
+        }
+        issued_k = T + 1;
+        wait(sh.v8_empty[sv], ((T / Cfg::kV8Stages) & 1) ^ 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&sh.v8_full[sv]);
+          const uint32_t dst = smem_u32(smem + Cfg::kOffV8 + sv * Cfg::kKBytes);
+          mbar_arrive_expect_tx(bar, Cfg::kKBytes);
+          tma_load_2d(dst, &tmV, bar, 0, y0, policy);
+          tma_load_2d(dst + Cfg::kKBytes / 2, &tmV, bar, 0, y1, policy);
+        }
+        issued_v = T + 1;
+      }
+      __syncwarp();
+      if (lane == 0) done_piece(n);
+    }
+    // every copy has landed before the CTA goes
+    for (int t = max(issued_k - Cfg::kKStages, 0); t < issued_k; ++t)
+      mbar_wait_bounded(smem_u32(&sh.k_full[t % Cfg::kKStages]), (t / Cfg::kKStages) & 1, p.wait_ns);
+    for (int t = max(issued_v - Cfg::kV8Stages, 0); t < issued_v; ++t)
+      mbar_wait_bounded(smem_u32(&sh.v8_full[t % Cfg::kV8Stages]), (t / Cfg::kV8Stages) & 1, p.wait_ns);
+  } else if (warp == kMmaWarp1) {
+    // ---- the issuing thread.  Each group is at its own place: the next
+    // thing it waits for is either its weights (then P V) or the end of its
+    // last P V (then the next Q K^T, which writes over those weights).  Both
+    // are polled, so neither group holds up the other.
+    if (lane == 0) {
+      constexpr uint32_t idesc_s = instr_desc_e4m3_f32(kGroupRows, kTilesN);
+      constexpr uint32_t idesc_o = idesc_f16_bmn(kGroupRows, kDim);
+      struct State {
+        int piece, j, tiles, groups, T;  // piece, tile within it, tile of this CTA
+        int used, pieces;                // tiles and pieces this group took part in
+        bool want_s, end;
+      } g[2];
+      auto enter = [&](State& s) {
+        const Piece& w = next_piece(s.piece);
+        s.end = !ok || w.last;
+        if (!s.end) {
+          s.j = 0;
+          s.tiles = w.tiles;
+          s.groups = w.groups;
+          s.want_s = true;
+        }
+      };
+      for (int i = 0; i < 2; ++i) {
+        g[i].piece = g[i].T = g[i].used = g[i].pieces = 0;
+        enter(g[i]);
+      }
+      uint64_t t0 = global_timer_ns();
+      uint32_t idle = 0;
+      while (ok && !(g[0].end && g[1].end)) {
+        bool moved = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          State& s = g[i];
+          if (s.end) continue;
+          const bool on = i < s.groups;
+          const int sk = s.T % Cfg::kKStages, so = s.T % Cfg::kVhStages;
+          if (s.want_s) {
+            if (!mbar_test(smem_u32(&sh.k_full[sk]), (s.T / Cfg::kKStages) & 1)) continue;
+            if (on) {
+              if (s.j == 0 && !mbar_test(smem_u32(&sh.q_full[i]), s.pieces & 1)) continue;
+              if (s.used > 0 && !mbar_test(smem_u32(&sh.o_done[i]), (s.used - 1) & 1)) continue;
+              tc_fence_after();
+              const uint32_t kb = smem_u32(smem + Cfg::kOffK + sk * Cfg::kKBytes);
+              const uint32_t qb = smem_u32(smem + 2 * i * Cfg::kQBytes);
+#pragma unroll
+              for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                for (int k = 0; k < kDim / 32; ++k)
+                  mma_e4m3_ss(tmem + 128 * i, desc_k_major<kDim>(qb + t * Cfg::kQBytes + 32 * k),
+                              desc_k_major<kDim>(kb + 32 * k), idesc_s, t + k > 0);
+              }
+              tc_commit1(smem_u32(&sh.s_full[i]));
+              tc_commit1(smem_u32(&sh.k_empty[sk]));
+            } else {
+              mbar_arrive(smem_u32(&sh.k_empty[sk]));
+            }
+            s.want_s = false;
+            moved = true;
+          } else {
+            if (on && !mbar_test(smem_u32(&sh.p_full[i]), s.used & 1)) continue;
+            if (!mbar_test(smem_u32(&sh.vh_full[so]), (s.T / Cfg::kVhStages) & 1)) continue;
+            if (on) {
+              tc_fence_after();
+              const uint32_t vb = smem_u32(smem + Cfg::kOffVh + so * Cfg::kVhBytes);
+#pragma unroll
+              for (int k = 0; k < kTilesN / 16; ++k)
+                mma_f16_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * k, desc_mn_major(vb + 2048 * k), idesc_o,
+                           s.j > 0 || k > 0);
+              tc_commit1(smem_u32(&sh.o_done[i]));
+              tc_commit1(smem_u32(&sh.vh_empty[so]));
+              ++s.used;
+            } else {
+              mbar_arrive(smem_u32(&sh.vh_empty[so]));
+            }
+            ++s.T;
+            s.want_s = true;
+            moved = true;
+            if (++s.j == s.tiles) {
+              if (on) ++s.pieces;
+              const bool other_past = g[1 - i].end || g[1 - i].piece > s.piece;
+              if (other_past) done_piece(s.piece);
+              ++s.piece;
+              enter(s);
+            }
+          }
+        }
+        if (moved) {
+          idle = 0;
+        } else if ((++idle & 1023u) == 0) {
+          const uint64_t now = global_timer_ns();
+          if (idle == 1024u) t0 = now;
+          if (now - t0 > p.wait_ns) {
+            ok = false;
+            atomicOr(p.err, kErrWaitContext);
+          }
+        }
+      }
+      // all products have completed before tensor memory is freed
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (g[i].used > 0) mbar_wait_bounded(smem_u32(&sh.o_done[i]), (g[i].used - 1) & 1, p.wait_ns);
+    }
+    __syncwarp();
+  }
+  } else if (warp >= kConvWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
+    // ---- V's codes to float16: a key per thread; both layouts keep a key's
+    // row together and swizzle its 16-byte chunks by the row, so eight
+    // threads read and write all banks
+    const int key = threadIdx.x - kConvWarp0 * 32;
+    int T = 0;
+    for (int n = 0; ok; ++n) {
+      const Piece& w = next_piece(n);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok || w.last) break;
+      const int tile0 = w.tile0, tiles = w.tiles, len = w.len;
+      for (int j = 0; j < tiles && ok; ++j, ++T) {
+        const int sv = T % Cfg::kV8Stages, so = T % Cfg::kVhStages;
+        wait(sh.v8_full[sv], (T / Cfg::kV8Stages) & 1);
+        wait(sh.vh_empty[so], ((T / Cfg::kVhStages) & 1) ^ 1);
+        const uint8_t* src = smem + Cfg::kOffV8 + sv * Cfg::kKBytes + key * Cfg::kRow;
+        uint8_t* dst = smem + Cfg::kOffVh + so * Cfg::kVhBytes + key * 128;
+        const bool there = (tile0 + j) * kTilesN + key < len;  // behind the last token: zeros, whatever is there
+#pragma unroll
+        for (int c = 0; c < kDim / 16; ++c) {
+          const int at = kDim == 128 ? (c ^ (key & 7)) << 4 : (c ^ ((key >> 1) & 3)) << 4;
+          uint4 v = *reinterpret_cast<const uint4*>(src + at);
+          if (!there) v = make_uint4(0, 0, 0, 0);
+          const uint4 lo = make_uint4(e4m3x2_to_half2(v.x), e4m3x2_to_half2(v.x >> 16), e4m3x2_to_half2(v.y), e4m3x2_to_half2(v.y >> 16));
+          const uint4 hi = make_uint4(e4m3x2_to_half2(v.z), e4m3x2_to_half2(v.z >> 16), e4m3x2_to_half2(v.w), e4m3x2_to_half2(v.w >> 16));
+          uint8_t* d = dst + (c >> 2) * (kTilesN * 128);
+          const int o = 2 * (c & 3);
+          *reinterpret_cast<uint4*>(d + ((o ^ (key & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(d + (((o + 1) ^ (key & 7)) << 4)) = hi;
+        }
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&sh.vh_full[so]));
+          mbar_arrive(smem_u32(&sh.v8_empty[sv]));
+        }
+      }
+      __syncwarp();
+      if (lane == 0) done_piece(n);
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ---- softmax: one thread per row
+    const int gi = (warp - kSoftWarp0) >> 2;
+    const int quarter = warp & 3;
+    const int row = gi * kGroupRows + quarter * 32 + lane;   // of the item
+    const uint32_t lanes = static_cast<uint32_t>(quarter * 32) << 16;
+    const uint32_t t_s = tmem + lanes + 128 * gi, t_o = tmem + lanes + 256 + 128 * gi;
+    uint8_t* q1 = smem + 2 * gi * Cfg::kQBytes;
+    uint8_t* q2 = q1 + Cfg::kQBytes;
+    int T = 0, used = 0, splits = 0;
+    float fac = 0.f;
+    Row o = {};
+    auto begin_piece = [&](const Piece& w) {
+      o = row_of(p, w, row);
+      fac = prepare_q<kDim>(p, o, q1, q2, row - gi * kGroupRows);
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[gi]));
+    };
+    {
+      const Piece& w = next_piece(0);
+      if (ok && !w.last && gi < w.groups) begin_piece(w);
+    }
+    for (int n = 0;; ++n) {
+      const Piece w = next_piece(n);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok || w.last) break;
+      const Row mine = o;
+      const bool on = gi < w.groups;
+      float m = -FLT_MAX, l = 0.f;
+      if (!on) {
+        T += w.tiles;
+      } else {
+        for (int j = 0; j < w.tiles; ++j, ++T, ++used) {
+          wait(sh.s_full[gi], used & 1);
+          wait(sh.sc_full[T % kScaleSlots], (T / kScaleSlots) & 1);
+          tc_fence_after();
+          const float4 sc = sh.scale[T % kScaleSlots];
+          const int key0 = (w.tile0 + j) * kTilesN;
+          uint32_t u[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, u[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_wait(u[c]);
+          float s[kTilesN];
+#pragma unroll
+          for (int i = 0; i < kTilesN; ++i) s[i] = __uint_as_float(u[i / 32][i % 32]);
+          const bool all = mine.lo <= key0 && mine.hi >= key0 + kTilesN - 1 && sc.x > 0.f && sc.z > 0.f;
+          if (!__all_sync(0xffffffffu, all)) {
+            const int lo = mine.lo - key0, span = mine.hi - mine.lo;
+#pragma unroll
+            for (int i = 0; i < kTilesN; ++i) {
+              const bool seen = mine.hi >= mine.lo && static_cast<uint32_t>(i - lo) <= static_cast<uint32_t>(span) &&
+                                (i < DG_PAGE ? sc.x : sc.z) > 0.f;
+              s[i] = seen ? s[i] : -INFINITY;
+            }
+          }
+          float c0 = fmaxf(fac * fabsf(sc.x), FLT_MIN), c1 = fmaxf(fac * fabsf(sc.z), FLT_MIN);
+          float a0 = s[0], a1 = s[DG_PAGE];
+#pragma unroll
+          for (int i = 1; i < DG_PAGE; ++i) {
+            a0 = fmaxf(a0, s[i]);
+            a1 = fmaxf(a1, s[DG_PAGE + i]);
+          }
+          // The weights take s c - m in one fused step, m being the rounded
+          // maximum: a difference that is off by up to 2^-24 |m|, the same for
+          // the whole row, and so of no effect until it nears the weights'
+          // headroom.  Logits that large are rounded first.
+          float top = fmaxf(__fmul_rn(a0, c0) + sc.y, __fmul_rn(a1, c1) + sc.w);
+          float lazy = kLazyLog2;
+          if (__any_sync(0xffffffffu, fabsf(top) > 4194304.f && top > -INFINITY)) {
+#pragma unroll
+            for (int i = 0; i < kTilesN; ++i) s[i] *= i < DG_PAGE ? c0 : c1;
+            c0 = c1 = 1.f;
+            lazy = 0.f;
+          }
+          const bool move = top > m + lazy;
+          if (__any_sync(0xffffffffu, move)) {
+            const float mn = move ? top : m;
+            const float shrink = exp2f(m - mn);
+            m = mn;
+            l *= shrink;
+            if (j > 0) {  // O holds the tiles before; their last product has to be done
+              wait(sh.o_done[gi], (used - 1) & 1);
+              tc_fence_after();
+#pragma unroll
+              for (int c = 0; c < kDim / 32; ++c) {
+                uint32_t x[32];
+                tmem_ld32(t_o + 32 * c, x);
+                tmem_ld_wait(x);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * shrink);
+                tmem_st32(t_o + 32 * c, x);
+              }
+            }
+          }
+          const float b0 = sc.y - m + kWeightLog2, b1 = sc.w - m + kWeightLog2;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            uint32_t h[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float x = exp2_fast(fmaf(s[64 * c + 2 * i], c ? c1 : c0, c ? b1 : b0));
+              const float y = exp2_fast(fmaf(s[64 * c + 2 * i + 1], c ? c1 : c0, c ? b1 : b0));
+              if (c) l1 += x + y; else l0 += x + y;
+              h[i] = pack_half2(x, y);
+            }
+            tmem_st32(t_s + 32 * c, h);
+          }
+          tmem_st_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[gi]));
+          l += l0 * pow2i(-static_cast<int>(sc.y)) + l1 * pow2i(-static_cast<int>(sc.w));
+        }
+      }
+      // the next piece's queries, so that its first product runs while this
+      // piece's result is written
+      {
+        const Piece& next = next_piece(n + 1);
+        if (ok && !next.last && gi < next.groups) begin_piece(next);
+      }
+      const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (static_cast<int>(blockIdx.x) == w.c0 ? 1 : 0);
+      auto store_lse = [&](float top, float sum) {
+        if (p.lse != nullptr && mine.live)
+          p.lse[mine.token * (static_cast<int64_t>(p.kv_heads) * p.group) + mine.head] =
+              sum == 0.f ? -INFINITY : (top - kWeightLog2 + log2f(sum)) * kLn2;
+      };
+      uint8_t* dst = p.out + mine.token * p.out_row + mine.head * p.out_head;
+      if (on) {
+        wait(sh.o_done[gi], (used - 1) & 1);
+        tc_fence_after();
+        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        float* part = p.part + slot * Cfg::kPartFloats;
+#pragma unroll
+        for (int c = 0; c < kDim / 32; ++c) {
+          uint32_t x[32];
+          tmem_ld32(t_o + 32 * c, x);
+          tmem_ld_wait(x);
+          if (w.whole) {
+            if (mine.live) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                uint32_t b[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const __nv_bfloat162 v = __floats2bfloat162_rn(__uint_as_float(x[8 * k + 2 * i]) * inv,
+                                                                 __uint_as_float(x[8 * k + 2 * i + 1]) * inv);
+                  b[i] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+                *reinterpret_cast<uint4*>(dst + 64 * c + 16 * k) = make_uint4(b[0], b[1], b[2], b[3]);
+              }
+            }
+          } else {  // [dim / 4][256] float4: a warp writes 512 bytes in a row
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              reinterpret_cast<uint4*>(part)[(8 * c + k) * kTilesM + row] =
+                  make_uint4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+          }
+        }
+        tc_fence_before();
+        if (w.whole) {
+          store_lse(m, l);
+        } else {
+          part[kTilesM * kDim + row] = m;
+          part[kTilesM * kDim + kTilesM + row] = l;
+        }
+      }
+      __syncwarp();
+      if (lane == 0) done_piece(n);
+      if (!w.whole) {
+        // the CTA that finishes an item's last part joins them, in split
+        // order; its warps meet on barriers whose waits are bounded too
+        __threadfence();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.parts_written));
+        if (warp == kSoftWarp0) {
+          wait(sh.parts_written, splits & 1);
+          if (lane == 0) {
+            const uint32_t before = atomicAdd(p.tickets + w.c0, 1u);
+            sh.last_part = before + 1 == static_cast<uint32_t>(w.parts);
+            if (sh.last_part) p.tickets[w.c0] = 0;
+            __threadfence();
+            mbar_arrive(smem_u32(&sh.last_known));
+          }
+          __syncwarp();
+        }
+        if (on) {
+          wait(sh.last_known, splits & 1);
+          if (ok && sh.last_part) {
+            auto part_of = [&](int i) {
+              return p.part + static_cast<size_t>(2 * (w.c0 + i) + (i == 0 ? 1 : 0)) * Cfg::kPartFloats;
+            };
+            float top = -FLT_MAX, sum = 0.f;
+            for (int i = 0; i < w.parts; ++i) top = fmaxf(top, __ldcg(part_of(i) + kTilesM * kDim + row));
+            for (int i = 0; i < w.parts; ++i) {
+              const float* src = part_of(i) + kTilesM * kDim;
+              sum += __ldcg(src + kTilesM + row) * join_weight(__ldcg(src + row), top);
+            }
+            const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+            for (int c = 0; c < kDim / 16; ++c) {
+              float x[16] = {};
+              for (int i = 0; i < w.parts; ++i) {
+                const float* src = part_of(i);
+                const float f = join_weight(__ldcg(src + kTilesM * kDim + row), top);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + (4 * c + k) * kTilesM + row);
+                  x[4 * k] += v.x * f;
+                  x[4 * k + 1] += v.y * f;
+                  x[4 * k + 2] += v.z * f;
+                  x[4 * k + 3] += v.w * f;
+                }
+              }
+              if (mine.live) {
+                uint32_t b[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                  const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i] * inv, x[2 * i + 1] * inv);
+                  b[i] = *reinterpret_cast<const uint32_t*>(&v);
+                }
+                *reinterpret_cast<uint4*>(dst + 32 * c) = make_uint4(b[0], b[1], b[2], b[3]);
+                *reinterpret_cast<uint4*>(dst + 32 * c + 16) = make_uint4(b[4], b[5], b[6], b[7]);
+              }
+            }
+            store_lse(top, sum);
+          }
+        }
+        ++splits;
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == kMmaWarp1) tmem_dealloc1(tmem, 512);
+}
+
+template <int kDim>
+int grid_of() {
+  static PerDevice<int> cache;
+  int dev = -1, n = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return -1;
+  const bool got = cache.get(dev, [](int* v) {
+    if (cudaFuncSetAttribute(attention_tiles_kernel<kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             TilesCfg<kDim>::kSmem) != cudaSuccess)
+      return false;
+    int per_sm = 0;
+    const int sms = device_sms();
+    if (sms <= 0 || cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attention_tiles_kernel<kDim>, kTilesThreads,
+                                                                  TilesCfg<kDim>::kSmem) != cudaSuccess || per_sm < 1)
+      return false;
+    *v = sms;
+    return true;
+  }, &n);
+  return got ? n : -1;
+}
+
+}  // namespace
+
+int tiles_grid(int dim) { return dim == 128 ? grid_of<128>() : grid_of<64>(); }
+size_t tiles_part_floats(int dim) { return dim == 128 ? TilesCfg<128>::kPartFloats : TilesCfg<64>::kPartFloats; }
+
+cudaError_t launch_attention_tiles(int dim, const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& p,
+                                   int grid, cudaStream_t stream) {
+  if (dim == 128)
+    attention_tiles_kernel<128><<<grid, kTilesThreads, TilesCfg<128>::kSmem, stream>>>(tmK, tmV, p);
+  else
+    attention_tiles_kernel<64><<<grid, kTilesThreads, TilesCfg<64>::kSmem, stream>>>(tmK, tmV, p);
+  return cudaGetLastError();
+}
+
+}  // namespace dg

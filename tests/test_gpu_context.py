@@ -12,8 +12,11 @@ fp16 2^-11, fp32 2^-24):
              sum w |v|: weights are rounded to float16 (2^-11; those under
              2^-24 of the largest are off by up to 2^-35 of it instead, which
              these inputs' sums stay above), and a logit
-             is off by at most d = (dim + 4) 2^-24 max sum |q k| (float32 sums),
-             which moves a weight and the normaliser by that part.
+             is off by at most d = (dim + 4) 2^-24 max sum |q k| (float32 sums)
+             + 2^-17 max |q| max sum |k| (queries as two E4M3 terms: an
+             element under 2^-9 of the largest is off by half the smallest
+             E4M3 step, 2^-10, when the largest is in [2^7, 2^8)), which moves
+             a weight and the normaliser by that part.
 """
 import math
 
@@ -309,7 +312,8 @@ def check_attention(plan, cache, q, causal, window=0, scale=None, max_new=0, ws=
             else:
                 lo = max(0, lens[r] - nq + i - window + 1) if window else 0
                 w, lw, mass, size = oc.attention(qs[i:i + 1], k[lo:], v[lo:], s, False, 0)
-            d = (dim + 4) * 2.0 ** -24 * size[0][:, None]
+            terms = 2.0 ** -17 * s * np.abs(qs[i]).max(-1, keepdims=True) * np.abs(k).sum(-1).max(initial=0)
+            d = (dim + 4) * 2.0 ** -24 * size[0][:, None] + terms
             tol = 2.0 ** -8 * np.abs(w[0]) + (2.0 ** -11 + 2.0 ** -20 + 2 * d) * mass[0] + 1e-38
             err = np.abs(o[start[r] + i] - w[0])
             assert np.all(err <= tol), (r, i, float((err / tol).max()))

@@ -71,7 +71,8 @@ def test_blocks_over_a_context():
                   .cpu().numpy()[page].transpose(0, 2, 1, 3).reshape(-1, kv, dim)[:n] for m in ("k", "v"))
         w, _, mass, size = oc.attention(q[r * L + i:r * L + i + 1].cpu().double().numpy(), kk, vv, dim ** -0.5, False, 0)
         err = np.abs(out[r * L + i].cpu().double().numpy() - w[0])
-        d = (dim + 4) * 2.0 ** -24 * size[0][:, None]
+        d = ((dim + 4) * 2.0 ** -24 * size[0][:, None] + 2.0 ** -17 * dim ** -0.5 * np.abs(kk).sum(-1).max() *
+             q[r * L + i].abs().amax(-1, keepdim=True).cpu().double().numpy())
         # Beside the bound of test_gpu_context.py: float16 weights go up to 2^10 in steps of 2^-24 at the
         # least, so a weight far below the largest is off by up to 2^-25 / 2^10 = 2^-35 of it, times its
         # code (at most 448) and page scale.  It shows here: in some columns every token with weight has
