@@ -1,8 +1,8 @@
 // context_tiles.cu -- attention over the 8-bit paged cache for many rows per
 // kv head (canvases, prompts), on the 5th-generation tensor cores.
 //
-// A CTA works on 256 packed query rows (two groups of 128) by 128 keys (two
-// pages).  Per tile and group:
+// A CTA works on 256 packed query rows (two groups of 128) by 64 keys (a
+// page).  Per tile and group:
 //   S = Q K^T   tcgen05.mma kind::f8f6f4, K's codes as the cache holds them
 //               and Q as two E4M3 terms q = (q1 + q2) 2^-e per row, which
 //               is exact for every element down to 2^-9 of the row's largest
@@ -29,22 +29,26 @@ namespace {
 
 constexpr int kGroupRows = 128;
 constexpr int kTilesM = 2 * kGroupRows;
-constexpr int kTilesN = 2 * DG_PAGE;  // keys per tile
+// Keys per tile.  Tensor memory has 256 columns for a group: O takes 128 (at
+// dim 128), so S has 128, and P lies over S.  With tiles of 128 keys the next
+// S has to wait for P V of this one, and products and softmax take turns
+// (measured: 6200 cycles for 256 rows x 128 keys); two S of 64 keys each let
+// the next product run under this tile's softmax, at the price of a Q operand
+// that is read twice as often.
+constexpr int kTilesN = DG_PAGE;
 constexpr float kWeightLog2 = 6.f;
 constexpr float kLazyLog2 = 8.f;      // the maximum may be exceeded by 2^8 before it moves
 
 // Warp roles.  Tensor memory is read by lane quarter (warp % 4), so each
-// softmax group is four consecutive warps; the issuing thread sits in the
-// lowest warp, which the schedulers favour.
-constexpr int kMmaWarp1 = 0, kLoadWarp = 1, kPlanWarp = 2;  // warp 3 is idle
+// softmax group is four consecutive warps.  Each group has an issuing warp of
+// its own: one thread serving both had to poll their barriers, and was late
+// for each by the time the other took.
+constexpr int kMmaWarp0 = 0, kLoadWarp = 2, kPlanWarp = 3;  // issuing warps 0 and 1
 constexpr int kSoftWarp0 = 4, kConvWarp0 = 12;
 constexpr int kTilesThreads = 512;
-// Registers: 512 threads x 128 at launch; the softmax warps hold a row of S.
-constexpr int kSoftRegs = 192, kOtherRegs = 64;
-static_assert(256 * kSoftRegs + 256 * kOtherRegs <= 512 * 128, "register split exceeds the launch's");
 
-constexpr int kScaleSlots = 8;  // tiles whose page scales are kept
-constexpr int kPieceSlots = 8;  // pieces of work known ahead; the groups are at most kKStages tiles apart
+constexpr int kScaleSlots = 16;  // tiles whose page scales are kept
+constexpr int kPieceSlots = 8;   // pieces of work known ahead; the groups are at most kKStages tiles apart
 
 template <int kDim>
 struct TilesCfg {
@@ -52,13 +56,13 @@ struct TilesCfg {
   static constexpr int kQBytes = kGroupRows * kRow;             // one term of one group
   static constexpr int kKBytes = kTilesN * kRow;
   static constexpr int kVhBytes = kTilesN * kDim * 2;
-  static constexpr int kKStages = kDim == 128 ? 3 : 4, kV8Stages = kDim == 128 ? 2 : 4, kVhStages = 2;
+  static constexpr int kKStages = 6, kV8Stages = 4, kVhStages = 4;
   static constexpr int kOffK = 4 * kQBytes;
   static constexpr int kOffV8 = kOffK + kKStages * kKBytes;
   static constexpr int kOffVh = kOffV8 + kV8Stages * kKBytes;
   static constexpr int kSmem = kOffVh + kVhStages * kVhBytes + 1024;
   static constexpr int kPartFloats = kTilesM * (kDim + 2);
-  static_assert(kKStages < kPieceSlots && kKStages < kScaleSlots - 1, "slots are written before they are read");
+  static_assert(kKStages < kPieceSlots && kKStages < kScaleSlots - 2, "slots are written before they are read");
   static_assert(kSmem <= 220 * 1024, "attention tiles exceed the shared memory of an SM");
 };
 
@@ -74,9 +78,9 @@ struct Piece {
 struct TilesShared {
   int64_t before[DG_MAX_B + 1];
   Piece piece[kPieceSlots];
-  float4 scale[kScaleSlots];  // (k scale, value exponent) of the tile's two pages; k scale < 0: page not there
-  uint64_t k_full[4], k_empty[4], v8_full[4], v8_empty[4], vh_full[2], vh_empty[2];
-  uint64_t q_full[2], s_full[2], p_full[2], o_done[2];
+  float2 scale[kScaleSlots];  // (k scale, value exponent) of the tile's page; k scale < 0: page not there
+  uint64_t k_full[6], k_empty[6], v8_full[4], v8_empty[4], vh_full[4], vh_empty[4];
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2];  // [group], [group][S buffer]
   uint64_t parts_written, last_known;
   uint64_t sc_full[kScaleSlots], piece_full[kPieceSlots], piece_empty[kPieceSlots];
   uint32_t tmem;
@@ -94,20 +98,27 @@ DG_DEV void tmem_dealloc1(uint32_t addr, uint32_t cols) {
 DG_DEV void tc_commit1(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+// The descriptors come as two 32-bit halves, the low one carrying the start
+// address: stepping along K or to another stage is then one 32-bit add of a
+// constant.  The issuing thread has 64 cycles per instruction; with 64-bit
+// descriptors put together on the spot it took 140 to 200.
 // D[tmem] (+)= A[smem] B[smem]^T, E4M3, both K-major (K = 32).
-DG_DEV void mma_e4m3_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+DG_DEV void mma_e4m3_ss(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc,
+                        uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "mov.b64 da, {%1, %2};\n\tmov.b64 db, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %5, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // D[tmem] (+)= A[tmem] B[smem], float16 (K = 16).
-DG_DEV void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+DG_DEV void mma_f16_ts(uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %5, 0;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate)
       : "memory");
 }
 // 32 consecutive 32-bit columns of this thread's tensor-memory lane.
@@ -134,27 +145,28 @@ DG_DEV void tmem_ld_wait(uint32_t (&r)[32]) {
                :
                : "memory");
 }
+// The same for 16 columns, and their stores.
+DG_DEV void tmem_ld16(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+               : "r"(addr)
+               : "memory");
+}
+DG_DEV void tmem_ld_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
+}
+DG_DEV void tmem_st16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+               : "memory");
+}
 DG_DEV void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};" ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+               : "memory");
 }
 DG_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-DG_DEV bool mbar_test(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
 
 // Descriptor of a K-major tile whose rows are one swizzle span (128 or 64
 // bytes), 8-row groups one after another.
@@ -197,6 +209,40 @@ DG_DEV uint32_t pack_half2(float lo, float hi) {
   return d;
 }
 
+// Two float32 lanes in one 64-bit register pair.
+DG_DEV uint64_t pack2(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+DG_DEV void unpack2(uint64_t v, float& x, float& y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+DG_DEV uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+DG_DEV uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+DG_DEV float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+DG_DEV float max_of_64(const float* s) {
+  float m[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+  for (int i = 4; i < 60; i += 8) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = max3(m[k], s[i + 2 * k], s[i + 2 * k + 1]);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], s[60 + k]);
+  return fmaxf(max3(m[0], m[1], m[2]), m[3]);
+}
+
 // A row's place in the batch.
 struct Row {
   bool live;
@@ -204,12 +250,12 @@ struct Row {
   int64_t token, head;   // row of the batch, query head
 };
 DG_DEV Row row_of(const AttnParams& p, const Piece& w, int row) {
-  const int64_t rho = static_cast<int64_t>(w.mt) * kTilesM + row;
-  const int i = static_cast<int>(rho / p.group);
+  const uint32_t rho = static_cast<uint32_t>(w.mt) * kTilesM + row;  // rows * group is below 2^31
+  const int i = static_cast<int>(rho / static_cast<uint32_t>(p.group));
   Row o;
   o.live = i < w.nq;
   o.token = w.row0 + i;
-  o.head = static_cast<int64_t>(w.h) * p.group + rho % p.group;
+  o.head = w.h * p.group + static_cast<int>(rho - i * p.group);
   Request q;
   q.nq = w.nq;
   q.len = w.len;
@@ -219,36 +265,40 @@ DG_DEV Row row_of(const AttnParams& p, const Piece& w, int row) {
   return o;
 }
 
-// This thread's query row as two E4M3 terms into shared memory (K-major,
-// swizzled); returns the factor that turns a dot product of the terms into a
-// logit in units of log2.
+// A warp's 32 query rows (from packed row rho0 of the piece) as two E4M3
+// terms into shared memory (K-major, swizzled).  Returns, to the thread of
+// each row, the factor that turns a dot product of the terms into a logit in
+// units of log2.  A row is read by dim / 8 neighbouring lanes, 16 bytes
+// each.
 template <int kDim>
-DG_DEV float prepare_q(const AttnParams& p, const Row& o, uint8_t* q1, uint8_t* q2, int row) {
-  uint4 w[kDim / 8];
-  const uint8_t* src = p.q + o.token * p.q_row + o.head * p.q_head;
-#pragma unroll
-  for (int c = 0; c < kDim / 8; ++c) w[c] = o.live ? *reinterpret_cast<const uint4*>(src + 16 * c) : make_uint4(0, 0, 0, 0);
-  // the largest magnitude, as an integer maximum over the bf16 halves
-  uint32_t top = 0;
-#pragma unroll
-  for (int c = 0; c < kDim / 8; ++c) {
-    const uint32_t u[4] = {w[c].x, w[c].y, w[c].z, w[c].w};
+DG_DEV float prepare_q(const AttnParams& p, const Piece& w, uint32_t rho0, uint8_t* q1, uint8_t* q2, int row0) {
+  constexpr int kLanes = kDim / 8;           // lanes per row
+  constexpr int kAtOnce = 32 / kLanes;       // rows per step
+  const int lane = threadIdx.x & 31, sub = lane / kLanes, c = lane % kLanes;
+  float mine = 1.f;
+#pragma unroll 8
+  for (int k = 0; k < 32 / kAtOnce; ++k) {
+    const int r = k * kAtOnce + sub;
+    const uint32_t rho = rho0 + r, i = rho / static_cast<uint32_t>(p.group);
+    const uint32_t head = w.h * p.group + (rho - i * p.group);
+    uint4 v = make_uint4(0, 0, 0, 0);
+    if (static_cast<int>(i) < w.nq)
+      v = *reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(w.row0 + i) * p.q_row + head * p.q_head + 16 * c);
+    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    uint32_t top = 0;  // the largest magnitude: float32 bits of the bf16 halves, as integers
 #pragma unroll
     for (int j = 0; j < 4; ++j) top = max(max(top, (u[j] << 16) & 0x7FFFFFFFu), u[j] & 0x7FFF0000u);
-  }
-  const int b = static_cast<int>(top >> 23);
-  const int e = b == 0 ? 0 : min(7 - (b - 127), 120);  // largest magnitude to [2^7, 2^8)
-  const bool finite = b < 255;
-  const float f = pow2i(e);
 #pragma unroll
-  for (int c = 0; c < kDim / 16; ++c) {
-    uint32_t t1[4], t2[4];
+    for (int d = kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const int b = static_cast<int>(top >> 23);
+    const int e = b == 0 ? 0 : min(7 - (b - 127), 120);  // largest magnitude to [2^7, 2^8)
+    const bool finite = b < 255;
+    const float f = pow2i(e);
+    uint32_t t1[2], t2[2];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint4 v = w[2 * c + (j >> 1)];
-      const uint32_t a = (j & 1) ? v.z : v.x, d = (j & 1) ? v.w : v.y;
-      const float x[4] = {__uint_as_float(a << 16) * f, __uint_as_float(a & 0xFFFF0000u) * f,
-                          __uint_as_float(d << 16) * f, __uint_as_float(d & 0xFFFF0000u) * f};
+    for (int j = 0; j < 2; ++j) {
+      const float x[4] = {__uint_as_float(u[2 * j] << 16) * f, __uint_as_float(u[2 * j] & 0xFFFF0000u) * f,
+                          __uint_as_float(u[2 * j + 1] << 16) * f, __uint_as_float(u[2 * j + 1] & 0xFFFF0000u) * f};
       const uint32_t lo = f2_to_e4m3x2(x[0], x[1]), hi = f2_to_e4m3x2(x[2], x[3]);
       const uint32_t hl = e4m3x2_to_half2(lo), hh = e4m3x2_to_half2(hi);
       const float2 bl = __half22float2(*reinterpret_cast<const __half2*>(&hl));
@@ -256,11 +306,17 @@ DG_DEV float prepare_q(const AttnParams& p, const Row& o, uint8_t* q1, uint8_t* 
       t1[j] = finite ? (lo | hi << 16) : 0x7F7F7F7Fu;  // a row that is not finite: NaN throughout
       t2[j] = f2_to_e4m3x2(x[0] - bl.x, x[1] - bl.y) | f2_to_e4m3x2(x[2] - bh.x, x[3] - bh.y) << 16;
     }
-    const int at = kDim == 128 ? row * 128 + ((c ^ (row & 7)) << 4) : row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
-    *reinterpret_cast<uint4*>(q1 + at) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-    *reinterpret_cast<uint4*>(q2 + at) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+    const int row = row0 + r, chunk = c >> 1;
+    const int at = (kDim == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4) : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4)) +
+                   8 * (c & 1);
+    *reinterpret_cast<uint2*>(q1 + at) = make_uint2(t1[0], t1[1]);
+    *reinterpret_cast<uint2*>(q2 + at) = make_uint2(t2[0], t2[1]);
+    // row r's factor is known to its lanes; thread r of the warp wants it
+    const float fac = finite ? p.scale_log2 * pow2i(-e) : 1.f;
+    const float got = __shfl_sync(0xffffffffu, fac, (lane % kAtOnce) * kLanes);
+    if (lane / kAtOnce == k) mine = got;
   }
-  return finite ? p.scale_log2 * pow2i(-e) : 1.f;
+  return mine;
 }
 
 template <int kDim>
@@ -275,22 +331,28 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < 4; ++s) {
+    for (int s = 0; s < Cfg::kKStages; ++s) {
       mbar_init(smem_u32(&sh.k_full[s]), 1);
       mbar_init(smem_u32(&sh.k_empty[s]), 2);
+    }
+    for (int s = 0; s < Cfg::kV8Stages; ++s) {
       mbar_init(smem_u32(&sh.v8_full[s]), 1);
       mbar_init(smem_u32(&sh.v8_empty[s]), 4);
     }
-    for (int s = 0; s < kPieceSlots; ++s) {
-      mbar_init(smem_u32(&sh.piece_full[s]), 1);
-      mbar_init(smem_u32(&sh.piece_empty[s]), 14);  // issuer, loader, 4 converter and 8 softmax warps
-    }
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < Cfg::kVhStages; ++s) {
       mbar_init(smem_u32(&sh.vh_full[s]), 4);
       mbar_init(smem_u32(&sh.vh_empty[s]), 2);
+    }
+    for (int s = 0; s < kPieceSlots; ++s) {
+      mbar_init(smem_u32(&sh.piece_full[s]), 1);
+      mbar_init(smem_u32(&sh.piece_empty[s]), 15);  // 2 issuing warps, loader, 4 converter and 8 softmax warps
+    }
+    for (int s = 0; s < 2; ++s) {
       mbar_init(smem_u32(&sh.q_full[s]), 4);
-      mbar_init(smem_u32(&sh.s_full[s]), 1);
-      mbar_init(smem_u32(&sh.p_full[s]), 4);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(smem_u32(&sh.s_full[s][b]), 1);
+        mbar_init(smem_u32(&sh.p_full[s][b]), 4);
+      }
       mbar_init(smem_u32(&sh.o_done[s]), 1);
     }
     for (int s = 0; s < kScaleSlots; ++s) mbar_init(smem_u32(&sh.sc_full[s]), 1);
@@ -298,7 +360,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     mbar_init(smem_u32(&sh.last_known), 1);
     fence_mbarrier_init();
   }
-  if (warp == kMmaWarp1) {
+  if (warp == kMmaWarp0) {
     tmem_alloc1(smem_u32(&sh.tmem), 512);
     tmem_relinquish1();
   }
@@ -307,7 +369,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  // columns: S (and P over it) of group g at 128 g, O at 256 + 128 g
+  // columns: S (and P over it) of group g, buffer b at 128 g + 64 b, O at 256 + 128 g
   const int64_t total = sh.before[p.B];
   const int64_t even = (total + gridDim.x - 1) / gridDim.x;
   const int64_t per = even > p.min_tiles ? even : p.min_tiles;
@@ -328,10 +390,6 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     mbar_arrive(smem_u32(&sh.piece_empty[n % kPieceSlots]));
   };
 
-  // A warpgroup's four warps change their registers together, so the roles
-  // are told apart by warpgroup first.
-  if (warp < kSoftWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
   if (warp == kPlanWarp) {
     // ---- the pieces of this CTA's range, some ahead of their use
     int64_t pos = blockIdx.x * per;
@@ -375,15 +433,15 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       const Piece& w = next_piece(n);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok || w.last) break;
-      const int page0 = 2 * w.tile0, pages = 2 * w.tiles;
       const int last_page = (w.len + DG_PAGE - 1) / DG_PAGE - 1;
       int id = 0;
       float ks = 0.f, ve = 0.f;
-      for (int j = 0; j < w.tiles && ok; ++j, ++T) {
-        if ((j & 15) == 0) {  // ids and scales of the next 32 pages, one per lane
-          const int m = 2 * j + lane, pg = page0 + m;
+      for (int j = 0; j < w.tiles; ++j, ++T) {
+        if ((j & 31) == 0) {  // ids and scales of the next 32 pages, one per lane
+          const int pg = w.tile0 + j + lane;
           id = -1;
-          if (m < pages && pg <= last_page && pg < p.max_pages) id = p.table[static_cast<size_t>(w.r) * p.max_pages + pg];
+          if (j + lane < w.tiles && pg <= last_page && pg < p.max_pages)
+            id = p.table[static_cast<size_t>(w.r) * p.max_pages + pg];
           if (id < 0 || id >= p.pages) {
             id = p.pages;  // outside the tensor: the copy fills zeros
             ks = -1.f;     // and its keys are not seen
@@ -394,25 +452,21 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
             ve = static_cast<float>(static_cast<int>(__float_as_uint(p.v_scale[at]) >> 23) - 127);
           }
         }
-        const int a = (2 * j) & 31;
-        const int id0 = __shfl_sync(0xffffffffu, id, a), id1 = __shfl_sync(0xffffffffu, id, a + 1);
-        const float ks0 = __shfl_sync(0xffffffffu, ks, a), ks1 = __shfl_sync(0xffffffffu, ks, a + 1);
-        const float ve0 = __shfl_sync(0xffffffffu, ve, a), ve1 = __shfl_sync(0xffffffffu, ve, a + 1);
-        const int y0 = (id0 * p.kv_heads + w.h) * DG_PAGE, y1 = (id1 * p.kv_heads + w.h) * DG_PAGE;
+        const int y = (__shfl_sync(0xffffffffu, id, j & 31) * p.kv_heads + w.h) * DG_PAGE;
+        const float ks_j = __shfl_sync(0xffffffffu, ks, j & 31), ve_j = __shfl_sync(0xffffffffu, ve, j & 31);
         const int st = T % Cfg::kKStages, sv = T % Cfg::kV8Stages;
         wait(sh.k_empty[st], ((T / Cfg::kKStages) & 1) ^ 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
-          // slot T % 8 was last read for tile T - 8; with K stage T % kKStages
-          // free, every softmax warp is past tile T - kKStages - 1
-          sh.scale[T % kScaleSlots] = make_float4(ks0, ve0, ks1, ve1);
+          // The slot was last read for tile T - kScaleSlots.  With K stage T %
+          // kKStages free, both groups have begun tile T - kKStages, and so
+          // every softmax warp is past tile T - kKStages - 2.
+          sh.scale[T % kScaleSlots] = make_float2(ks_j, ve_j);
           mbar_arrive(smem_u32(&sh.sc_full[T % kScaleSlots]));
           const uint32_t bar = smem_u32(&sh.k_full[st]);
-          const uint32_t dst = smem_u32(smem + Cfg::kOffK + st * Cfg::kKBytes);
           mbar_arrive_expect_tx(bar, Cfg::kKBytes);
-          tma_load_2d(dst, &tmK, bar, 0, y0, policy);
-          tma_load_2d(dst + Cfg::kKBytes / 2, &tmK, bar, 0, y1, policy);
+          tma_load_2d(smem_u32(smem + Cfg::kOffK + st * Cfg::kKBytes), &tmK, bar, 0, y, policy);
         }
         issued_k = T + 1;
         wait(sh.v8_empty[sv], ((T / Cfg::kV8Stages) & 1) ^ 1);
@@ -420,10 +474,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         if (!ok) break;
         if (lane == 0) {
           const uint32_t bar = smem_u32(&sh.v8_full[sv]);
-          const uint32_t dst = smem_u32(smem + Cfg::kOffV8 + sv * Cfg::kKBytes);
           mbar_arrive_expect_tx(bar, Cfg::kKBytes);
-          tma_load_2d(dst, &tmV, bar, 0, y0, policy);
-          tma_load_2d(dst + Cfg::kKBytes / 2, &tmV, bar, 0, y1, policy);
+          tma_load_2d(smem_u32(smem + Cfg::kOffV8 + sv * Cfg::kKBytes), &tmV, bar, 0, y, policy);
         }
         issued_v = T + 1;
       }
@@ -435,117 +487,102 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       mbar_wait_bounded(smem_u32(&sh.k_full[t % Cfg::kKStages]), (t / Cfg::kKStages) & 1, p.wait_ns);
     for (int t = max(issued_v - Cfg::kV8Stages, 0); t < issued_v; ++t)
       mbar_wait_bounded(smem_u32(&sh.v8_full[t % Cfg::kV8Stages]), (t / Cfg::kV8Stages) & 1, p.wait_ns);
-  } else if (warp == kMmaWarp1) {
-    // ---- the issuing thread.  Each group is at its own place: the next
-    // thing it waits for is either its weights (then P V) or the end of its
-    // last P V (then the next Q K^T, which writes over those weights).  Both
-    // are polled, so neither group holds up the other.
-    if (lane == 0) {
-      constexpr uint32_t idesc_s = instr_desc_e4m3_f32(kGroupRows, kTilesN);
-      constexpr uint32_t idesc_o = idesc_f16_bmn(kGroupRows, kDim);
-      struct State {
-        int piece, j, tiles, groups, T;  // piece, tile within it, tile of this CTA
-        int used, pieces;                // tiles and pieces this group took part in
-        bool want_s, end;
-      } g[2];
-      auto enter = [&](State& s) {
-        const Piece& w = next_piece(s.piece);
-        s.end = !ok || w.last;
-        if (!s.end) {
-          s.j = 0;
-          s.tiles = w.tiles;
-          s.groups = w.groups;
-          s.want_s = true;
+  } else if (warp < kMmaWarp0 + 2) {
+    // ---- the issuing warps: the next tile's S = Q K^T ahead of this tile's
+    // O += P V
+    const int gi = warp - kMmaWarp0;
+    constexpr uint32_t idesc_s = instr_desc_e4m3_f32(kGroupRows, kTilesN);
+    constexpr uint32_t idesc_o = idesc_f16_bmn(kGroupRows, kDim);
+    const uint64_t q0 = desc_k_major<kDim>(smem_u32(smem + 2 * gi * Cfg::kQBytes));
+    const uint64_t k0 = desc_k_major<kDim>(smem_u32(smem + Cfg::kOffK)), v0 = desc_mn_major(smem_u32(smem + Cfg::kOffVh));
+    const uint32_t q_lo = static_cast<uint32_t>(q0), k_lo = static_cast<uint32_t>(k0), v_lo = static_cast<uint32_t>(v0);
+    const uint32_t k_hi = static_cast<uint32_t>(k0 >> 32), v_hi = static_cast<uint32_t>(v0 >> 32);
+    const uint32_t t_s = tmem + 128 * gi, t_o = tmem + 256 + 128 * gi;
+    uint32_t sk = 0, pk = 0, sv = 0, pv = 0;
+    uint32_t a = 0, b = 0;  // products S and P V issued so far (mod 2^32)
+    uint32_t pieces = 0;
+    for (int n = 0; ok; ++n) {
+      const Piece& w = next_piece(n);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok || w.last) break;
+      const int tiles = w.tiles;
+      const bool on = gi < w.groups;
+      auto score = [&](bool first) {
+        wait(sh.k_full[sk], pk);
+        if (on) {
+          if (first) wait(sh.q_full[gi], pieces & 1);
+          // The buffer is free once P V of two tiles back is done.  A piece's
+          // first S comes after the last P V before it, any other ahead of the
+          // P V in between; o_done is never more than one phase further.
+          if (first) {
+            if (b > 0) wait(sh.o_done[gi], (b - 1) & 1);
+          } else if (a >= 2) {
+            wait(sh.o_done[gi], (a - 2) & 1);
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        if (lane == 0) {
+          if (on) {
+            tc_fence_after();
+            const uint32_t kb = k_lo + sk * (Cfg::kKBytes >> 4), d = t_s + 64 * (a & 1);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+#pragma unroll
+              for (int k = 0; k < kDim / 32; ++k)
+                mma_e4m3_ss(d, q_lo + t * (Cfg::kQBytes >> 4) + 2 * k, k_hi, kb + 2 * k, k_hi, idesc_s, t + k > 0);
+            }
+            tc_commit1(smem_u32(&sh.s_full[gi][a & 1]));
+            tc_commit1(smem_u32(&sh.k_empty[sk]));
+          } else {
+            mbar_arrive(smem_u32(&sh.k_empty[sk]));
+          }
+        }
+        __syncwarp();
+        if (on) ++a;
+        if (++sk == Cfg::kKStages) {
+          sk = 0;
+          pk ^= 1;
         }
       };
-      for (int i = 0; i < 2; ++i) {
-        g[i].piece = g[i].T = g[i].used = g[i].pieces = 0;
-        enter(g[i]);
-      }
-      uint64_t t0 = global_timer_ns();
-      uint32_t idle = 0;
-      while (ok && !(g[0].end && g[1].end)) {
-        bool moved = false;
+      score(true);
+      for (int j = 0; j < tiles && ok; ++j) {
+        if (j + 1 < tiles) score(false);
+        if (on) wait(sh.p_full[gi][b & 1], (b >> 1) & 1);
+        wait(sh.vh_full[sv], pv);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          if (on) {
+            tc_fence_after();
+            const uint32_t vb = v_lo + sv * (Cfg::kVhBytes >> 4), s = t_s + 64 * (b & 1);
+            mma_f16_ts(t_o, s, vb, v_hi, idesc_o, j > 0);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          State& s = g[i];
-          if (s.end) continue;
-          const bool on = i < s.groups;
-          const int sk = s.T % Cfg::kKStages, so = s.T % Cfg::kVhStages;
-          if (s.want_s) {
-            if (!mbar_test(smem_u32(&sh.k_full[sk]), (s.T / Cfg::kKStages) & 1)) continue;
-            if (on) {
-              if (s.j == 0 && !mbar_test(smem_u32(&sh.q_full[i]), s.pieces & 1)) continue;
-              if (s.used > 0 && !mbar_test(smem_u32(&sh.o_done[i]), (s.used - 1) & 1)) continue;
-              tc_fence_after();
-              const uint32_t kb = smem_u32(smem + Cfg::kOffK + sk * Cfg::kKBytes);
-              const uint32_t qb = smem_u32(smem + 2 * i * Cfg::kQBytes);
-#pragma unroll
-              for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int k = 0; k < kDim / 32; ++k)
-                  mma_e4m3_ss(tmem + 128 * i, desc_k_major<kDim>(qb + t * Cfg::kQBytes + 32 * k),
-                              desc_k_major<kDim>(kb + 32 * k), idesc_s, t + k > 0);
-              }
-              tc_commit1(smem_u32(&sh.s_full[i]));
-              tc_commit1(smem_u32(&sh.k_empty[sk]));
-            } else {
-              mbar_arrive(smem_u32(&sh.k_empty[sk]));
-            }
-            s.want_s = false;
-            moved = true;
+            for (int k = 1; k < kTilesN / 16; ++k) mma_f16_ts(t_o, s + 8 * k, vb + 128 * k, v_hi, idesc_o, 1u);
+            tc_commit1(smem_u32(&sh.o_done[gi]));
+            tc_commit1(smem_u32(&sh.vh_empty[sv]));
           } else {
-            if (on && !mbar_test(smem_u32(&sh.p_full[i]), s.used & 1)) continue;
-            if (!mbar_test(smem_u32(&sh.vh_full[so]), (s.T / Cfg::kVhStages) & 1)) continue;
-            if (on) {
-              tc_fence_after();
-              const uint32_t vb = smem_u32(smem + Cfg::kOffVh + so * Cfg::kVhBytes);
-#pragma unroll
-              for (int k = 0; k < kTilesN / 16; ++k)
-                mma_f16_ts(tmem + 256 + 128 * i, tmem + 128 * i + 8 * k, desc_mn_major(vb + 2048 * k), idesc_o,
-                           s.j > 0 || k > 0);
-              tc_commit1(smem_u32(&sh.o_done[i]));
-              tc_commit1(smem_u32(&sh.vh_empty[so]));
-              ++s.used;
-            } else {
-              mbar_arrive(smem_u32(&sh.vh_empty[so]));
-            }
-            ++s.T;
-            s.want_s = true;
-            moved = true;
-            if (++s.j == s.tiles) {
-              if (on) ++s.pieces;
-              const bool other_past = g[1 - i].end || g[1 - i].piece > s.piece;
-              if (other_past) done_piece(s.piece);
-              ++s.piece;
-              enter(s);
-            }
+            mbar_arrive(smem_u32(&sh.vh_empty[sv]));
           }
         }
-        if (moved) {
-          idle = 0;
-        } else if ((++idle & 1023u) == 0) {
-          const uint64_t now = global_timer_ns();
-          if (idle == 1024u) t0 = now;
-          if (now - t0 > p.wait_ns) {
-            ok = false;
-            atomicOr(p.err, kErrWaitContext);
-          }
+        __syncwarp();
+        if (on) ++b;
+        if (++sv == Cfg::kVhStages) {
+          sv = 0;
+          pv ^= 1;
         }
       }
-      // all products have completed before tensor memory is freed
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        if (g[i].used > 0) mbar_wait_bounded(smem_u32(&sh.o_done[i]), (g[i].used - 1) & 1, p.wait_ns);
+      if (on) ++pieces;
+      if (ok && lane == 0) done_piece(n);
     }
-    __syncwarp();
-  }
+    // its products have completed before tensor memory is freed
+    if (a > b) mbar_wait_bounded(smem_u32(&sh.s_full[gi][(a - 1) & 1]), ((a - 1) >> 1) & 1, p.wait_ns);
+    if (b > 0) mbar_wait_bounded(smem_u32(&sh.o_done[gi]), (b - 1) & 1, p.wait_ns);
   } else if (warp >= kConvWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegs));
-    // ---- V's codes to float16: a key per thread; both layouts keep a key's
+    // ---- V's codes to float16: half a key per thread; both layouts keep a key's
     // row together and swizzle its 16-byte chunks by the row, so eight
     // threads read and write all banks
-    const int key = threadIdx.x - kConvWarp0 * 32;
+    const int tid = threadIdx.x - kConvWarp0 * 32, key = tid & 63, side = tid >> 6;
     int T = 0;
     for (int n = 0; ok; ++n) {
       const Piece& w = next_piece(n);
@@ -560,7 +597,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         uint8_t* dst = smem + Cfg::kOffVh + so * Cfg::kVhBytes + key * 128;
         const bool there = (tile0 + j) * kTilesN + key < len;  // behind the last token: zeros, whatever is there
 #pragma unroll
-        for (int c = 0; c < kDim / 16; ++c) {
+        for (int i = 0; i < kDim / 32; ++i) {
+          const int c = side * (kDim / 32) + i;
           const int at = kDim == 128 ? (c ^ (key & 7)) << 4 : (c ^ ((key >> 1) & 3)) << 4;
           uint4 v = *reinterpret_cast<const uint4*>(src + at);
           if (!there) v = make_uint4(0, 0, 0, 0);
@@ -582,7 +620,6 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       if (lane == 0) done_piece(n);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
     // ---- softmax: one thread per row
     const int gi = (warp - kSoftWarp0) >> 2;
     const int quarter = warp & 3;
@@ -593,10 +630,12 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     uint8_t* q2 = q1 + Cfg::kQBytes;
     int T = 0, used = 0, splits = 0;
     float fac = 0.f;
-    Row o = {};
+    int key_first = 1, key_last = 0;  // the keys this thread's row sees
     auto begin_piece = [&](const Piece& w) {
-      o = row_of(p, w, row);
-      fac = prepare_q<kDim>(p, o, q1, q2, row - gi * kGroupRows);
+      const Row o = row_of(p, w, row);
+      key_first = o.lo;
+      key_last = o.hi;
+      fac = prepare_q<kDim>(p, w, w.mt * kTilesM + gi * kGroupRows + quarter * 32, q1, q2, quarter * 32);
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[gi]));
@@ -606,56 +645,52 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       if (ok && !w.last && gi < w.groups) begin_piece(w);
     }
     for (int n = 0;; ++n) {
-      const Piece w = next_piece(n);
+      const Piece& w = next_piece(n);  // in shared memory until done_piece
       ok = __all_sync(0xffffffffu, ok);
       if (!ok || w.last) break;
-      const Row mine = o;
       const bool on = gi < w.groups;
+      const int tile0 = w.tile0, tiles = w.tiles;
       float m = -FLT_MAX, l = 0.f;
       if (!on) {
-        T += w.tiles;
+        T += tiles;
       } else {
-        for (int j = 0; j < w.tiles; ++j, ++T, ++used) {
-          wait(sh.s_full[gi], used & 1);
+        for (int j = 0; j < tiles; ++j, ++T, ++used) {
+          const uint32_t t_p = t_s + 64 * (used & 1);
+          wait(sh.s_full[gi][used & 1], (used >> 1) & 1);
           wait(sh.sc_full[T % kScaleSlots], (T / kScaleSlots) & 1);
           tc_fence_after();
-          const float4 sc = sh.scale[T % kScaleSlots];
-          const int key0 = (w.tile0 + j) * kTilesN;
-          uint32_t u[4][32];
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, u[c]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld_wait(u[c]);
+          const float2 sc = sh.scale[T % kScaleSlots];
+          const int key0 = (tile0 + j) * kTilesN;
           float s[kTilesN];
+          {
+            uint32_t u[2][32];
+            tmem_ld32(t_p, u[0]);
+            tmem_ld32(t_p + 32, u[1]);
+            tmem_ld_wait(u[0]);
+            tmem_ld_wait(u[1]);
 #pragma unroll
-          for (int i = 0; i < kTilesN; ++i) s[i] = __uint_as_float(u[i / 32][i % 32]);
-          const bool all = mine.lo <= key0 && mine.hi >= key0 + kTilesN - 1 && sc.x > 0.f && sc.z > 0.f;
+            for (int i = 0; i < kTilesN; ++i) s[i] = __uint_as_float(u[i / 32][i % 32]);
+          }
+          const bool all = key_first <= key0 && key_last >= key0 + kTilesN - 1 && sc.x > 0.f;
           if (!__all_sync(0xffffffffu, all)) {
-            const int lo = mine.lo - key0, span = mine.hi - mine.lo;
+            const int lo = key_first - key0, span = sc.x > 0.f ? key_last - key_first : -1;
 #pragma unroll
             for (int i = 0; i < kTilesN; ++i) {
-              const bool seen = mine.hi >= mine.lo && static_cast<uint32_t>(i - lo) <= static_cast<uint32_t>(span) &&
-                                (i < DG_PAGE ? sc.x : sc.z) > 0.f;
+              const bool seen = span >= 0 && static_cast<uint32_t>(i - lo) <= static_cast<uint32_t>(span);
               s[i] = seen ? s[i] : -INFINITY;
             }
           }
-          float c0 = fmaxf(fac * fabsf(sc.x), FLT_MIN), c1 = fmaxf(fac * fabsf(sc.z), FLT_MIN);
-          float a0 = s[0], a1 = s[DG_PAGE];
-#pragma unroll
-          for (int i = 1; i < DG_PAGE; ++i) {
-            a0 = fmaxf(a0, s[i]);
-            a1 = fmaxf(a1, s[DG_PAGE + i]);
-          }
+          float c = fmaxf(fac * fabsf(sc.x), FLT_MIN);
           // The weights take s c - m in one fused step, m being the rounded
           // maximum: a difference that is off by up to 2^-24 |m|, the same for
           // the whole row, and so of no effect until it nears the weights'
           // headroom.  Logits that large are rounded first.
-          float top = fmaxf(__fmul_rn(a0, c0) + sc.y, __fmul_rn(a1, c1) + sc.w);
+          float top = __fmul_rn(max_of_64(s), c) + sc.y;
           float lazy = kLazyLog2;
           if (__any_sync(0xffffffffu, fabsf(top) > 4194304.f && top > -INFINITY)) {
 #pragma unroll
-            for (int i = 0; i < kTilesN; ++i) s[i] *= i < DG_PAGE ? c0 : c1;
-            c0 = c1 = 1.f;
+            for (int i = 0; i < kTilesN; ++i) s[i] *= c;
+            c = 1.f;
             lazy = 0.f;
           }
           const bool move = top > m + lazy;
@@ -667,36 +702,39 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
             if (j > 0) {  // O holds the tiles before; their last product has to be done
               wait(sh.o_done[gi], (used - 1) & 1);
               tc_fence_after();
-#pragma unroll
-              for (int c = 0; c < kDim / 32; ++c) {
-                uint32_t x[32];
-                tmem_ld32(t_o + 32 * c, x);
+#pragma unroll 1
+              for (int c16 = 0; c16 < kDim / 16; ++c16) {
+                uint32_t x[16];
+                tmem_ld16(t_o + 16 * c16, x);
                 tmem_ld_wait(x);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * shrink);
-                tmem_st32(t_o + 32 * c, x);
+                for (int i = 0; i < 16; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * shrink);
+                tmem_st16(t_o + 16 * c16, x);
               }
             }
           }
-          const float b0 = sc.y - m + kWeightLog2, b1 = sc.w - m + kWeightLog2;
-          float l0 = 0.f, l1 = 0.f;
+          const uint64_t cc = pack2(c, c);
+          const float off = sc.y - m + kWeightLog2;
+          const uint64_t bb = pack2(off, off);
+          uint64_t sum[4] = {0, 0, 0, 0};
+          uint32_t h[32];
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            uint32_t h[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float x = exp2_fast(fmaf(s[64 * c + 2 * i], c ? c1 : c0, c ? b1 : b0));
-              const float y = exp2_fast(fmaf(s[64 * c + 2 * i + 1], c ? c1 : c0, c ? b1 : b0));
-              if (c) l1 += x + y; else l0 += x + y;
-              h[i] = pack_half2(x, y);
-            }
-            tmem_st32(t_s + 32 * c, h);
+          for (int i = 0; i < 32; ++i) {
+            float x, y;
+            unpack2(fma2(pack2(s[2 * i], s[2 * i + 1]), cc, bb), x, y);
+            x = exp2_fast(x);
+            y = exp2_fast(y);
+            sum[i & 3] = add2(sum[i & 3], pack2(x, y));
+            h[i] = pack_half2(x, y);
           }
+          tmem_st32(t_p, h);
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[gi]));
-          l += l0 * pow2i(-static_cast<int>(sc.y)) + l1 * pow2i(-static_cast<int>(sc.w));
+          if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[gi][used & 1]));
+          float x, y;
+          unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
+          l += (x + y) * pow2i(-static_cast<int>(sc.y));
         }
       }
       // the next piece's queries, so that its first product runs while this
@@ -705,6 +743,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         const Piece& next = next_piece(n + 1);
         if (ok && !next.last && gi < next.groups) begin_piece(next);
       }
+      const Row mine = row_of(p, w, row);
       const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (static_cast<int>(blockIdx.x) == w.c0 ? 1 : 0);
       auto store_lse = [&](float top, float sum) {
         if (p.lse != nullptr && mine.live)
@@ -751,8 +790,6 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
           part[kTilesM * kDim + kTilesM + row] = l;
         }
       }
-      __syncwarp();
-      if (lane == 0) done_piece(n);
       if (!w.whole) {
         // the CTA that finishes an item's last part joins them, in split
         // order; its warps meet on barriers whose waits are bounded too
@@ -783,29 +820,35 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
               sum += __ldcg(src + kTilesM + row) * join_weight(__ldcg(src + row), top);
             }
             const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-            for (int c = 0; c < kDim / 16; ++c) {
-              float x[16] = {};
+            // 64 columns at a time: 16 reads in flight a thread
+#pragma unroll 1
+            for (int c = 0; c < kDim / 64; ++c) {
+              float x[64] = {};
               for (int i = 0; i < w.parts; ++i) {
                 const float* src = part_of(i);
+                float4 v[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(src) + (16 * c + k) * kTilesM + row);
                 const float f = join_weight(__ldcg(src + kTilesM * kDim + row), top);
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + (4 * c + k) * kTilesM + row);
-                  x[4 * k] += v.x * f;
-                  x[4 * k + 1] += v.y * f;
-                  x[4 * k + 2] += v.z * f;
-                  x[4 * k + 3] += v.w * f;
+                for (int k = 0; k < 16; ++k) {
+                  x[4 * k] += v[k].x * f;
+                  x[4 * k + 1] += v[k].y * f;
+                  x[4 * k + 2] += v[k].z * f;
+                  x[4 * k + 3] += v[k].w * f;
                 }
               }
               if (mine.live) {
-                uint32_t b[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                  const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i] * inv, x[2 * i + 1] * inv);
-                  b[i] = *reinterpret_cast<const uint32_t*>(&v);
+                for (int k = 0; k < 8; ++k) {
+                  uint32_t b[4];
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 v = __floats2bfloat162_rn(x[8 * k + 2 * i] * inv, x[8 * k + 2 * i + 1] * inv);
+                    b[i] = *reinterpret_cast<const uint32_t*>(&v);
+                  }
+                  *reinterpret_cast<uint4*>(dst + 128 * c + 16 * k) = make_uint4(b[0], b[1], b[2], b[3]);
                 }
-                *reinterpret_cast<uint4*>(dst + 32 * c) = make_uint4(b[0], b[1], b[2], b[3]);
-                *reinterpret_cast<uint4*>(dst + 32 * c + 16) = make_uint4(b[4], b[5], b[6], b[7]);
               }
             }
             store_lse(top, sum);
@@ -813,12 +856,14 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         }
         ++splits;
       }
+      __syncwarp();
+      if (lane == 0) done_piece(n);
     }
   }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == kMmaWarp1) tmem_dealloc1(tmem, 512);
+  if (warp == kMmaWarp0) tmem_dealloc1(tmem, 512);
 }
 
 template <int kDim>
