@@ -480,11 +480,11 @@ int rows_grid() {
   return got ? n : -1;
 }
 
-// Workspace: the fault latch, the tickets, the parts.  Sized for both
+// Workspace: the fault latch, the tickets, the split items, the parts.  Sized for both
 // kernels, so that one workspace serves every batch of a shape.
 struct AttnWs {
   int rows_grid, tiles_grid;
-  size_t tickets, part, total;
+  size_t tickets, splits, part, total;
 };
 bool attn_ws(int dim, AttnWs* w) {
   w->rows_grid = dim == 128 ? rows_grid<128>() : rows_grid<64>();
@@ -494,7 +494,9 @@ bool attn_ws(int dim, AttnWs* w) {
   const size_t a = static_cast<size_t>(w->rows_grid) * rows_floats, b = w->tiles_grid * tiles_part_floats(dim);
   const int grid = w->rows_grid > w->tiles_grid ? w->rows_grid : w->tiles_grid;
   w->tickets = kWsAlign;
-  w->part = w->tickets + (static_cast<size_t>(grid) * 4 + kWsAlign - 1) / kWsAlign * kWsAlign;
+  auto up = [](size_t n) { return (n + kWsAlign - 1) / kWsAlign * kWsAlign; };
+  w->splits = w->tickets + up(static_cast<size_t>(grid) * 4);
+  w->part = w->splits + up(static_cast<size_t>(grid) * tiles_split_bytes());
   w->total = w->part + 2 * sizeof(float) * (a > b ? a : b);
   return true;
 }
@@ -569,6 +571,7 @@ dg_status dg_context_attention(const dg_context* ctx, const dg_context_cache* ca
   uint8_t* wsb = static_cast<uint8_t*>(workspace);
   p.err = reinterpret_cast<uint32_t*>(wsb);
   p.tickets = reinterpret_cast<uint32_t*>(wsb + ws.tickets);
+  p.splits = wsb + ws.splits;
   p.part = reinterpret_cast<float*>(wsb + ws.part);
   p.wait_ns = kDefaultWaitNs;
 

@@ -31,7 +31,8 @@ struct AttnParams {
   int32_t window;
   // workspace
   float* part;        // [2 * grid][part_floats]
-  uint32_t* tickets;  // [grid], 0 between launches
+  uint32_t* tickets;  // [grid], 0 between launches (rows kernel)
+  void* splits;       // [grid] the split items (tiles kernel)
   uint32_t* err;
   uint64_t wait_ns;
   int32_t min_tiles;  // least tiles a CTA takes
@@ -203,9 +204,11 @@ DG_DEV float exp2_fast(float x) {
 }
 
 // The kernel for many rows (context_tiles.cu): its resident CTAs on the
-// current device (-1: none), the floats of one part, its launch.
+// current device (-1: none), the floats of one part, the bytes of one split
+// item, its launch.
 int tiles_grid(int dim);
 size_t tiles_part_floats(int dim);
+size_t tiles_split_bytes();
 cudaError_t launch_attention_tiles(int dim, const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& p,
                                    int grid, cudaStream_t stream);
 

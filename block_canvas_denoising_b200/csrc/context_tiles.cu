@@ -81,10 +81,8 @@ struct TilesShared {
   float2 scale[kScaleSlots];  // (k scale, value exponent) of the tile's page; k scale < 0: page not there
   uint64_t k_full[6], k_empty[6], v8_full[4], v8_empty[4], vh_full[4], vh_empty[4];
   uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2];  // [group], [group][S buffer]
-  uint64_t parts_written, last_known;
   uint64_t sc_full[kScaleSlots], piece_full[kPieceSlots], piece_empty[kPieceSlots];
   uint32_t tmem;
-  uint32_t last_part;
 };
 
 // ---- tcgen05 for a CTA on its own -----------------------------------------
@@ -167,6 +165,38 @@ DG_DEV void tmem_st32(uint32_t addr, const uint32_t (&r)[32]) {
                : "memory");
 }
 DG_DEV void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// mbarrier tests without the suspend hint: half the latency of the hinted
+// form when the phase is already over (48 cycles against 84), which is what a
+// chain of short waits on one path pays.
+DG_DEV uint32_t mbar_over(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok;
+}
+// Wait for both phases (the same barrier twice for one), for at most limit_ns.
+DG_DEV bool wait_over(uint32_t bar_a, uint32_t par_a, uint32_t bar_b, uint32_t par_b, uint64_t limit_ns) {
+  if (mbar_over(bar_a, par_a) & mbar_over(bar_b, par_b)) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_over(bar_a, par_a) & mbar_over(bar_b, par_b)) return true;
+    if ((i & 63u) == 0 && global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
+DG_DEV bool wait_over(uint32_t bar, uint32_t parity, uint64_t limit_ns) {
+  if (mbar_over(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+#pragma unroll 1
+  for (uint32_t i = 1;; ++i) {
+    if (mbar_over(bar, parity)) return true;
+    if ((i & 63u) == 0 && global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
 
 // Descriptor of a K-major tile whose rows are one swizzle span (128 or 64
 // bytes), 8-row groups one after another.
@@ -266,57 +296,77 @@ DG_DEV Row row_of(const AttnParams& p, const Piece& w, int row) {
 }
 
 // A warp's 32 query rows (from packed row rho0 of the piece) as two E4M3
-// terms into shared memory (K-major, swizzled).  Returns, to the thread of
-// each row, the factor that turns a dot product of the terms into a logit in
-// units of log2.  A row is read by dim / 8 neighbouring lanes, 16 bytes
-// each.
+// terms in shared memory (K-major, swizzled).  The bf16 rows come by
+// asynchronous copies, dim / 8 neighbouring lanes to a row, into the very
+// place of the two terms -- a row of bf16 is as long as both -- and every
+// thread then turns its own row: 16 reads in flight a lane and no shuffles.
+// Returns the factor that turns a dot product of the thread's row into a
+// logit in units of log2.
 template <int kDim>
 DG_DEV float prepare_q(const AttnParams& p, const Piece& w, uint32_t rho0, uint8_t* q1, uint8_t* q2, int row0) {
   constexpr int kLanes = kDim / 8;           // lanes per row
   constexpr int kAtOnce = 32 / kLanes;       // rows per step
   const int lane = threadIdx.x & 31, sub = lane / kLanes, c = lane % kLanes;
-  float mine = 1.f;
-#pragma unroll 8
+  // chunk i of a row: the first dim / 16 lie in q1, the others in q2
+  auto place = [&](int row, int i) {
+    const int k = i & (kDim / 16 - 1);
+    return (i < kDim / 16 ? q1 : q2) + (kDim == 128 ? row * 128 + ((k ^ (row & 7)) << 4) : row * 64 + ((k ^ ((row >> 1) & 3)) << 4));
+  };
+#pragma unroll 1
   for (int k = 0; k < 32 / kAtOnce; ++k) {
     const int r = k * kAtOnce + sub;
     const uint32_t rho = rho0 + r, i = rho / static_cast<uint32_t>(p.group);
     const uint32_t head = w.h * p.group + (rho - i * p.group);
-    uint4 v = make_uint4(0, 0, 0, 0);
-    if (static_cast<int>(i) < w.nq)
-      v = *reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(w.row0 + i) * p.q_row + head * p.q_head + 16 * c);
+    const bool live = static_cast<int>(i) < w.nq;
+    const uint8_t* src = p.q + (live ? static_cast<int64_t>(w.row0 + i) * p.q_row + head * p.q_head + 16 * c : 0);
+    // a row that is not there: nothing is read and the place is filled with zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(row0 + r, c))), "l"(src), "r"(live ? 16 : 0)
+                 : "memory");
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();
+  const int row = row0 + lane;
+  uint32_t top = 0;  // the largest magnitude: float32 bits of the bf16 halves, as integers
+#pragma unroll
+  for (int i = 0; i < kDim / 8; ++i) {
+    const uint4 v = *reinterpret_cast<const uint4*>(place(row, i));
     const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-    uint32_t top = 0;  // the largest magnitude: float32 bits of the bf16 halves, as integers
 #pragma unroll
     for (int j = 0; j < 4; ++j) top = max(max(top, (u[j] << 16) & 0x7FFFFFFFu), u[j] & 0x7FFF0000u);
-#pragma unroll
-    for (int d = kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const int b = static_cast<int>(top >> 23);
-    const int e = b == 0 ? 0 : min(7 - (b - 127), 120);  // largest magnitude to [2^7, 2^8)
-    const bool finite = b < 255;
-    const float f = pow2i(e);
-    uint32_t t1[2], t2[2];
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const float x[4] = {__uint_as_float(u[2 * j] << 16) * f, __uint_as_float(u[2 * j] & 0xFFFF0000u) * f,
-                          __uint_as_float(u[2 * j + 1] << 16) * f, __uint_as_float(u[2 * j + 1] & 0xFFFF0000u) * f};
-      const uint32_t lo = f2_to_e4m3x2(x[0], x[1]), hi = f2_to_e4m3x2(x[2], x[3]);
-      const uint32_t hl = e4m3x2_to_half2(lo), hh = e4m3x2_to_half2(hi);
-      const float2 bl = __half22float2(*reinterpret_cast<const __half2*>(&hl));
-      const float2 bh = __half22float2(*reinterpret_cast<const __half2*>(&hh));
-      t1[j] = finite ? (lo | hi << 16) : 0x7F7F7F7Fu;  // a row that is not finite: NaN throughout
-      t2[j] = f2_to_e4m3x2(x[0] - bl.x, x[1] - bl.y) | f2_to_e4m3x2(x[2] - bh.x, x[3] - bh.y) << 16;
-    }
-    const int row = row0 + r, chunk = c >> 1;
-    const int at = (kDim == 128 ? row * 128 + ((chunk ^ (row & 7)) << 4) : row * 64 + ((chunk ^ ((row >> 1) & 3)) << 4)) +
-                   8 * (c & 1);
-    *reinterpret_cast<uint2*>(q1 + at) = make_uint2(t1[0], t1[1]);
-    *reinterpret_cast<uint2*>(q2 + at) = make_uint2(t2[0], t2[1]);
-    // row r's factor is known to its lanes; thread r of the warp wants it
-    const float fac = finite ? p.scale_log2 * pow2i(-e) : 1.f;
-    const float got = __shfl_sync(0xffffffffu, fac, (lane % kAtOnce) * kLanes);
-    if (lane / kAtOnce == k) mine = got;
   }
-  return mine;
+  const int b = static_cast<int>(top >> 23);
+  const int e = b == 0 ? 0 : min(7 - (b - 127), 120);  // largest magnitude to [2^7, 2^8)
+  const bool finite = b < 255;
+  const float f = pow2i(e);
+  // Chunks 2i and 2i + 1 become chunk i of both terms.  The first term's
+  // place is chunk i, which has been read by then; the second's is not, and
+  // waits in registers.
+  uint4 second[kDim / 16];
+#pragma unroll
+  for (int i = 0; i < kDim / 16; ++i) {
+    uint32_t t1[4], t2[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint4 v = *reinterpret_cast<const uint4*>(place(row, 2 * i + h));
+      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float x[4] = {__uint_as_float(u[2 * j] << 16) * f, __uint_as_float(u[2 * j] & 0xFFFF0000u) * f,
+                            __uint_as_float(u[2 * j + 1] << 16) * f, __uint_as_float(u[2 * j + 1] & 0xFFFF0000u) * f};
+        const uint32_t lo = f2_to_e4m3x2(x[0], x[1]), hi = f2_to_e4m3x2(x[2], x[3]);
+        const uint32_t hl = e4m3x2_to_half2(lo), hh = e4m3x2_to_half2(hi);
+        const float2 bl = __half22float2(*reinterpret_cast<const __half2*>(&hl));
+        const float2 bh = __half22float2(*reinterpret_cast<const __half2*>(&hh));
+        t1[2 * h + j] = finite ? (lo | hi << 16) : 0x7F7F7F7Fu;  // a row that is not finite: NaN throughout
+        t2[2 * h + j] = f2_to_e4m3x2(x[0] - bl.x, x[1] - bl.y) | f2_to_e4m3x2(x[2] - bh.x, x[3] - bh.y) << 16;
+      }
+    }
+    *reinterpret_cast<uint4*>(place(row, i)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
+    second[i] = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+  }
+#pragma unroll
+  for (int i = 0; i < kDim / 16; ++i) *reinterpret_cast<uint4*>(place(row, kDim / 16 + i)) = second[i];
+  return finite ? p.scale_log2 * pow2i(-e) : 1.f;
 }
 
 template <int kDim>
@@ -356,8 +406,6 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       mbar_init(smem_u32(&sh.o_done[s]), 1);
     }
     for (int s = 0; s < kScaleSlots; ++s) mbar_init(smem_u32(&sh.sc_full[s]), 1);
-    mbar_init(smem_u32(&sh.parts_written), 8);
-    mbar_init(smem_u32(&sh.last_known), 1);
     fence_mbarrier_init();
   }
   if (warp == kMmaWarp0) {
@@ -369,6 +417,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may take its place
   // columns: S (and P over it) of group g, buffer b at 128 g + 64 b, O at 256 + 128 g
   const int64_t total = sh.before[p.B];
   const int64_t even = (total + gridDim.x - 1) / gridDim.x;
@@ -376,7 +425,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
 
   bool ok = true;
   auto wait = [&](uint64_t& bar, uint32_t parity) {
-    if (ok && !mbar_wait_bounded(smem_u32(&bar), parity, p.wait_ns)) {
+    if (ok && !wait_over(smem_u32(&bar), parity, p.wait_ns)) {
+      ok = false;
+      atomicOr(p.err, kErrWaitContext);
+    }
+  };
+  auto wait2 = [&](uint64_t& a, uint32_t pa, uint64_t& b, uint32_t pb) {
+    if (ok && !wait_over(smem_u32(&a), pa, smem_u32(&b), pb, p.wait_ns)) {
       ok = false;
       atomicOr(p.err, kErrWaitContext);
     }
@@ -394,6 +449,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     // ---- the pieces of this CTA's range, some ahead of their use
     int64_t pos = blockIdx.x * per;
     const int64_t end = min(pos + per, total);
+    Piece split = {};
     for (int n = 0; ok; ++n) {
       if (n >= kPieceSlots) wait(sh.piece_empty[n % kPieceSlots], ((n / kPieceSlots) & 1) ^ 1);
       ok = __all_sync(0xffffffffu, ok);
@@ -418,6 +474,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         w.c0 = static_cast<int>(it.begin / per);
         w.parts = static_cast<int>((item_end - 1) / per) - w.c0 + 1;
         pos += w.tiles;
+        if (!w.whole && w.c0 == static_cast<int>(blockIdx.x)) split = w;  // an item that begins here and ends elsewhere
       }
       if (lane == 0) {
         sh.piece[n % kPieceSlots] = w;
@@ -425,6 +482,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       }
       if (w.last) break;
     }
+    if (lane == 0) static_cast<Piece*>(p.splits)[blockIdx.x] = split;  // for the kernel that joins the parts
   } else if (warp == kLoadWarp) {
     // ---- copies of K and V codes, and the pages' scales
     const uint64_t policy = policy_evict_last();  // row tiles of a head share its keys
@@ -501,45 +559,37 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     uint32_t sk = 0, pk = 0, sv = 0, pv = 0;
     uint32_t a = 0, b = 0;  // products S and P V issued so far (mod 2^32)
     uint32_t pieces = 0;
-    for (int n = 0; ok; ++n) {
+    for (int n = 0; ok && lane == 0; ++n) {
       const Piece& w = next_piece(n);
-      ok = __all_sync(0xffffffffu, ok);
       if (!ok || w.last) break;
       const int tiles = w.tiles;
       const bool on = gi < w.groups;
       auto score = [&](bool first) {
-        wait(sh.k_full[sk], pk);
-        if (on) {
-          if (first) wait(sh.q_full[gi], pieces & 1);
-          // The buffer is free once P V of two tiles back is done.  A piece's
-          // first S comes after the last P V before it, any other ahead of the
-          // P V in between; o_done is never more than one phase further.
-          if (first) {
-            if (b > 0) wait(sh.o_done[gi], (b - 1) & 1);
-          } else if (a >= 2) {
-            wait(sh.o_done[gi], (a - 2) & 1);
-          }
-        }
-        ok = __all_sync(0xffffffffu, ok);
+        // The buffer is free once P V of two tiles back is done.  A piece's
+        // first S comes after the last P V before it, any other ahead of the P V
+        // in between; o_done is never more than one phase further.
+        if (on && first) wait(sh.q_full[gi], pieces & 1);
+        const uint32_t behind = first ? b - 1 : a - 2;
+        if (on && static_cast<int>(behind) >= 0)
+          wait2(sh.k_full[sk], pk, sh.o_done[gi], behind & 1);
+        else
+          wait(sh.k_full[sk], pk);
         if (!ok) return;
-        if (lane == 0) {
-          if (on) {
-            tc_fence_after();
-            const uint32_t kb = k_lo + sk * (Cfg::kKBytes >> 4), d = t_s + 64 * (a & 1);
+        if (on) {
+          tc_fence_after();
+          const uint32_t kb = k_lo + sk * (Cfg::kKBytes >> 4), d = t_s + 64 * (a & 1);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
+          for (int t = 0; t < 2; ++t) {
 #pragma unroll
-              for (int k = 0; k < kDim / 32; ++k)
-                mma_e4m3_ss(d, q_lo + t * (Cfg::kQBytes >> 4) + 2 * k, k_hi, kb + 2 * k, k_hi, idesc_s, t + k > 0);
-            }
-            tc_commit1(smem_u32(&sh.s_full[gi][a & 1]));
-            tc_commit1(smem_u32(&sh.k_empty[sk]));
-          } else {
-            mbar_arrive(smem_u32(&sh.k_empty[sk]));
+            for (int k = 0; k < kDim / 32; ++k)
+              mma_e4m3_ss(d, q_lo + t * (Cfg::kQBytes >> 4) + 2 * k, k_hi, kb + 2 * k, k_hi, idesc_s, t + k > 0);
           }
+          tc_commit1(smem_u32(&sh.s_full[gi][a & 1]));
+          tc_commit1(smem_u32(&sh.k_empty[sk]));
+          ++a;
+        } else {
+          mbar_arrive(smem_u32(&sh.k_empty[sk]));
         }
-        __syncwarp();
-        if (on) ++a;
         if (++sk == Cfg::kKStages) {
           sk = 0;
           pk ^= 1;
@@ -548,36 +598,35 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       score(true);
       for (int j = 0; j < tiles && ok; ++j) {
         if (j + 1 < tiles) score(false);
-        if (on) wait(sh.p_full[gi][b & 1], (b >> 1) & 1);
-        wait(sh.vh_full[sv], pv);
-        ok = __all_sync(0xffffffffu, ok);
+        if (on)
+          wait2(sh.p_full[gi][b & 1], (b >> 1) & 1, sh.vh_full[sv], pv);
+        else
+          wait(sh.vh_full[sv], pv);
         if (!ok) break;
-        if (lane == 0) {
-          if (on) {
-            tc_fence_after();
-            const uint32_t vb = v_lo + sv * (Cfg::kVhBytes >> 4), s = t_s + 64 * (b & 1);
-            mma_f16_ts(t_o, s, vb, v_hi, idesc_o, j > 0);
+        if (on) {
+          tc_fence_after();
+          const uint32_t vb = v_lo + sv * (Cfg::kVhBytes >> 4), s = t_s + 64 * (b & 1);
+          mma_f16_ts(t_o, s, vb, v_hi, idesc_o, j > 0);
 #pragma unroll
-            for (int k = 1; k < kTilesN / 16; ++k) mma_f16_ts(t_o, s + 8 * k, vb + 128 * k, v_hi, idesc_o, 1u);
-            tc_commit1(smem_u32(&sh.o_done[gi]));
-            tc_commit1(smem_u32(&sh.vh_empty[sv]));
-          } else {
-            mbar_arrive(smem_u32(&sh.vh_empty[sv]));
-          }
+          for (int k = 1; k < kTilesN / 16; ++k) mma_f16_ts(t_o, s + 8 * k, vb + 128 * k, v_hi, idesc_o, 1u);
+          tc_commit1(smem_u32(&sh.o_done[gi]));
+          tc_commit1(smem_u32(&sh.vh_empty[sv]));
+          ++b;
+        } else {
+          mbar_arrive(smem_u32(&sh.vh_empty[sv]));
         }
-        __syncwarp();
-        if (on) ++b;
         if (++sv == Cfg::kVhStages) {
           sv = 0;
           pv ^= 1;
         }
       }
       if (on) ++pieces;
-      if (ok && lane == 0) done_piece(n);
+      if (ok) done_piece(n);
     }
     // its products have completed before tensor memory is freed
     if (a > b) mbar_wait_bounded(smem_u32(&sh.s_full[gi][(a - 1) & 1]), ((a - 1) >> 1) & 1, p.wait_ns);
     if (b > 0) mbar_wait_bounded(smem_u32(&sh.o_done[gi]), (b - 1) & 1, p.wait_ns);
+    __syncwarp();
   } else if (warp >= kConvWarp0) {
     // ---- V's codes to float16: half a key per thread; both layouts keep a key's
     // row together and swizzle its 16-byte chunks by the row, so eight
@@ -628,7 +677,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     const uint32_t t_s = tmem + lanes + 128 * gi, t_o = tmem + lanes + 256 + 128 * gi;
     uint8_t* q1 = smem + 2 * gi * Cfg::kQBytes;
     uint8_t* q2 = q1 + Cfg::kQBytes;
-    int T = 0, used = 0, splits = 0;
+    int T = 0, used = 0;
     float fac = 0.f;
     int key_first = 1, key_last = 0;  // the keys this thread's row sees
     auto begin_piece = [&](const Piece& w) {
@@ -640,24 +689,24 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&sh.q_full[gi]));
     };
-    {
-      const Piece& w = next_piece(0);
-      if (ok && !w.last && gi < w.groups) begin_piece(w);
-    }
-    for (int n = 0;; ++n) {
-      const Piece& w = next_piece(n);  // in shared memory until done_piece
+    // Round n works on piece n, prepares the queries of piece n + 1 and writes
+    // the result of piece n; round -1 prepares only.  One place in the code
+    // for each: what runs once per piece runs from a cold instruction cache,
+    // and costs by its length.
+    for (int n = -1;; ++n) {
+      const Piece& w = n < 0 ? next_piece(0) : next_piece(n);  // in shared memory until done_piece
       ok = __all_sync(0xffffffffu, ok);
       if (!ok || w.last) break;
-      const bool on = gi < w.groups;
-      const int tile0 = w.tile0, tiles = w.tiles;
+      const bool on = n >= 0 && gi < w.groups;
+      const int tile0 = w.tile0, tiles = n < 0 ? 0 : w.tiles;
       float m = -FLT_MAX, l = 0.f;
       if (!on) {
         T += tiles;
       } else {
         for (int j = 0; j < tiles; ++j, ++T, ++used) {
           const uint32_t t_p = t_s + 64 * (used & 1);
-          wait(sh.s_full[gi][used & 1], (used >> 1) & 1);
-          wait(sh.sc_full[T % kScaleSlots], (T / kScaleSlots) & 1);
+          if (j == 0) wait(sh.s_full[gi][used & 1], (used >> 1) & 1);  // before scales: this warp may have skipped tiles
+          wait2(sh.s_full[gi][used & 1], (used >> 1) & 1, sh.sc_full[T % kScaleSlots], (T / kScaleSlots) & 1);
           tc_fence_after();
           const float2 sc = sh.scale[T % kScaleSlots];
           const int key0 = (tile0 + j) * kTilesN;
@@ -743,6 +792,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         const Piece& next = next_piece(n + 1);
         if (ok && !next.last && gi < next.groups) begin_piece(next);
       }
+      if (n < 0) continue;
       const Row mine = row_of(p, w, row);
       const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (static_cast<int>(blockIdx.x) == w.c0 ? 1 : 0);
       auto store_lse = [&](float top, float sum) {
@@ -756,7 +806,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         tc_fence_after();
         const float inv = l == 0.f ? 0.f : 1.0f / l;
         float* part = p.part + slot * Cfg::kPartFloats;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < kDim / 32; ++c) {
           uint32_t x[32];
           tmem_ld32(t_o + 32 * c, x);
@@ -790,72 +840,6 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
           part[kTilesM * kDim + kTilesM + row] = l;
         }
       }
-      if (!w.whole) {
-        // the CTA that finishes an item's last part joins them, in split
-        // order; its warps meet on barriers whose waits are bounded too
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.parts_written));
-        if (warp == kSoftWarp0) {
-          wait(sh.parts_written, splits & 1);
-          if (lane == 0) {
-            const uint32_t before = atomicAdd(p.tickets + w.c0, 1u);
-            sh.last_part = before + 1 == static_cast<uint32_t>(w.parts);
-            if (sh.last_part) p.tickets[w.c0] = 0;
-            __threadfence();
-            mbar_arrive(smem_u32(&sh.last_known));
-          }
-          __syncwarp();
-        }
-        if (on) {
-          wait(sh.last_known, splits & 1);
-          if (ok && sh.last_part) {
-            auto part_of = [&](int i) {
-              return p.part + static_cast<size_t>(2 * (w.c0 + i) + (i == 0 ? 1 : 0)) * Cfg::kPartFloats;
-            };
-            float top = -FLT_MAX, sum = 0.f;
-            for (int i = 0; i < w.parts; ++i) top = fmaxf(top, __ldcg(part_of(i) + kTilesM * kDim + row));
-            for (int i = 0; i < w.parts; ++i) {
-              const float* src = part_of(i) + kTilesM * kDim;
-              sum += __ldcg(src + kTilesM + row) * join_weight(__ldcg(src + row), top);
-            }
-            const float inv = sum == 0.f ? 0.f : 1.0f / sum;
-            // 64 columns at a time: 16 reads in flight a thread
-#pragma unroll 1
-            for (int c = 0; c < kDim / 64; ++c) {
-              float x[64] = {};
-              for (int i = 0; i < w.parts; ++i) {
-                const float* src = part_of(i);
-                float4 v[16];
-#pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = __ldcg(reinterpret_cast<const float4*>(src) + (16 * c + k) * kTilesM + row);
-                const float f = join_weight(__ldcg(src + kTilesM * kDim + row), top);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                  x[4 * k] += v[k].x * f;
-                  x[4 * k + 1] += v[k].y * f;
-                  x[4 * k + 2] += v[k].z * f;
-                  x[4 * k + 3] += v[k].w * f;
-                }
-              }
-              if (mine.live) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                  uint32_t b[4];
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 v = __floats2bfloat162_rn(x[8 * k + 2 * i] * inv, x[8 * k + 2 * i + 1] * inv);
-                    b[i] = *reinterpret_cast<const uint32_t*>(&v);
-                  }
-                  *reinterpret_cast<uint4*>(dst + 128 * c + 16 * k) = make_uint4(b[0], b[1], b[2], b[3]);
-                }
-              }
-            }
-            store_lse(top, sum);
-          }
-        }
-        ++splits;
-      }
       __syncwarp();
       if (lane == 0) done_piece(n);
     }
@@ -864,6 +848,59 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
   __syncthreads();
   tc_fence_after();
   if (warp == kMmaWarp0) tmem_dealloc1(tmem, 512);
+}
+
+// Joins the parts of the items that more than one CTA worked on, in split
+// order, so results do not depend on which CTA was done first.  Block (c, y)
+// works on the item that begins in CTA c's range and ends behind it, if there
+// is one; a warp on 32 rows x 16 elements, 4 reads of 16 bytes a lane and
+// part, four parts at once: for one canvas, 22 items in 7 parts of 133 KB each,
+// spread over the whole device (one CTA joining an item alone took 32 us).
+constexpr int kJoinThreads = 256;
+template <int kDim>
+__global__ void __launch_bounds__(kJoinThreads)
+attention_join_kernel(const __grid_constant__ AttnParams p) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kPartFloats = TilesCfg<kDim>::kPartFloats;
+  const Piece w = static_cast<const Piece*>(p.splits)[blockIdx.x];
+  if (w.parts < 2) return;
+  const int unit = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int row = (unit & 7) * 32 + lane, c = unit >> 3;  // 16 elements from 16 c
+  if (c >= kDim / 16) return;
+  const Row o = row_of(p, w, row);
+  if (!o.live) return;
+  auto part_of = [&](int i) { return p.part + static_cast<size_t>(2 * (w.c0 + i) + (i == 0 ? 1 : 0)) * kPartFloats; };
+  float top = -FLT_MAX;
+#pragma unroll 4
+  for (int i = 0; i < w.parts; ++i) top = fmaxf(top, __ldcg(part_of(i) + kTilesM * kDim + row));
+  float sum = 0.f, x[16] = {};
+#pragma unroll 4
+  for (int i = 0; i < w.parts; ++i) {
+    const float* src = part_of(i);
+    const float f = join_weight(__ldcg(src + kTilesM * kDim + row), top);
+    sum += __ldcg(src + kTilesM * kDim + kTilesM + row) * f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + (4 * c + k) * kTilesM + row);
+      x[4 * k] += v.x * f;
+      x[4 * k + 1] += v.y * f;
+      x[4 * k + 2] += v.z * f;
+      x[4 * k + 3] += v.w * f;
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  uint32_t b[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i] * inv, x[2 * i + 1] * inv);
+    b[i] = *reinterpret_cast<const uint32_t*>(&v);
+  }
+  uint4* dst = reinterpret_cast<uint4*>(p.out + o.token * p.out_row + o.head * p.out_head + 32 * c);
+  dst[0] = make_uint4(b[0], b[1], b[2], b[3]);
+  dst[1] = make_uint4(b[4], b[5], b[6], b[7]);
+  if (p.lse != nullptr && c == 0)
+    p.lse[o.token * (static_cast<int64_t>(p.kv_heads) * p.group) + o.head] =
+        sum == 0.f ? -INFINITY : (top - kWeightLog2 + log2f(sum)) * kLn2;
 }
 
 template <int kDim>
@@ -891,13 +928,30 @@ int grid_of() {
 int tiles_grid(int dim) { return dim == 128 ? grid_of<128>() : grid_of<64>(); }
 size_t tiles_part_floats(int dim) { return dim == 128 ? TilesCfg<128>::kPartFloats : TilesCfg<64>::kPartFloats; }
 
+size_t tiles_split_bytes() { return sizeof(Piece); }
+
+namespace {
+template <int kDim>
+cudaError_t launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& p, int grid, cudaStream_t stream) {
+  attention_tiles_kernel<kDim><<<grid, kTilesThreads, TilesCfg<kDim>::kSmem, stream>>>(tmK, tmV, p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid, kDim / 16);
+  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attention_join_kernel<kDim>, p);
+}
+}  // namespace
+
 cudaError_t launch_attention_tiles(int dim, const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& p,
                                    int grid, cudaStream_t stream) {
-  if (dim == 128)
-    attention_tiles_kernel<128><<<grid, kTilesThreads, TilesCfg<128>::kSmem, stream>>>(tmK, tmV, p);
-  else
-    attention_tiles_kernel<64><<<grid, kTilesThreads, TilesCfg<64>::kSmem, stream>>>(tmK, tmV, p);
-  return cudaGetLastError();
+  return dim == 128 ? launch<128>(tmK, tmV, p, grid, stream) : launch<64>(tmK, tmV, p, grid, stream);
 }
 
 }  // namespace dg
