@@ -37,7 +37,13 @@ constexpr int kTilesM = 2 * kGroupRows;
 // that is read twice as often.
 constexpr int kTilesN = DG_PAGE;
 constexpr float kWeightLog2 = 6.f;
+// Of a row's 32 pairs of weights, so many are exponentials by polynomial: the
+// special function unit gives 4 a cycle and scheduler, which is half of a
+// tile's time.  0 / 6 / 10 / 14 pairs: 277 / 267 / 275 / 281 us for a canvas
+// over 131072 tokens.
+constexpr int kPolyPairs = 6;
 constexpr float kLazyLog2 = 8.f;      // the maximum may be exceeded by 2^8 before it moves
+constexpr float kLargeLog2 = 4194304.f;  // 2^22
 
 // Warp roles.  Tensor memory is read by lane quarter (warp % 4), so each
 // softmax group is four consecutive warps.  Each group has an issuing warp of
@@ -256,22 +262,49 @@ DG_DEV uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
   return d;
 }
+// 2^x of two numbers up to 127 without the special function unit: the
+// nearest whole number n by adding 1.5 * 2^23, 2^(x - n) by the polynomial of
+// degree 4 with the least largest relative error on [-1/2, 1/2] (2.6e-6, found
+// by Remez exchange), n into the exponent.
+// Anything below, -inf too, gives about 2^-126: nothing in float16, and next to
+// nothing in a sum.
+DG_DEV void exp2_poly2(uint64_t v, float& x, float& y) {
+  float a, b;
+  unpack2(v, a, b);
+  const uint64_t w = pack2(fmaxf(a, -126.f), fmaxf(b, -126.f));
+  const uint64_t magic = pack2(12582912.f, 12582912.f), minus = pack2(-12582912.f, -12582912.f);
+  const uint64_t t = add2(w, magic);
+  const uint64_t f = fma2(add2(t, minus), pack2(-1.f, -1.f), w);
+  uint64_t q = fma2(f, pack2(0.009570102207362652f, 0.009570102207362652f), pack2(0.05591785907745361f, 0.05591785907745361f));
+  q = fma2(q, f, pack2(0.240247443318367f, 0.240247443318367f));
+  q = fma2(q, f, pack2(0.6931217908859253f, 0.6931217908859253f));
+  q = fma2(q, f, pack2(0.9999992847442627f, 0.9999992847442627f));
+  float qa, qb, ta, tb;
+  unpack2(q, qa, qb);
+  unpack2(t, ta, tb);
+  x = __uint_as_float(__float_as_uint(qa) + (__float_as_uint(ta) << 23));
+  y = __uint_as_float(__float_as_uint(qb) + (__float_as_uint(tb) << 23));
+}
 DG_DEV float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-DG_DEV float max_of_64(const float* s) {
-  float m[4] = {s[0], s[1], s[2], s[3]};
+DG_DEV float max_of_32(const uint32_t (&u)[32]) {
+  float m[4];
 #pragma unroll
-  for (int i = 4; i < 60; i += 8) {
+  for (int k = 0; k < 4; ++k) m[k] = fmaxf(__uint_as_float(u[k]), __uint_as_float(u[28 + k]));
 #pragma unroll
-    for (int k = 0; k < 4; ++k) m[k] = max3(m[k], s[i + 2 * k], s[i + 2 * k + 1]);
+  for (int i = 4; i < 28; i += 8) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m[k] = max3(m[k], __uint_as_float(u[i + 2 * k]), __uint_as_float(u[i + 2 * k + 1]));
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) m[k] = fmaxf(m[k], s[60 + k]);
   return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
+
+// A row that saw no key: its maximum never moved.  (A row of NaN has not
+// moved it either, but its sum is NaN.)
+DG_DEV bool saw_nothing(float m, float l) { return m == -FLT_MAX && l < 1.f; }
 
 // A row's place in the batch.
 struct Row {
@@ -312,16 +345,18 @@ DG_DEV float prepare_q(const AttnParams& p, const Piece& w, uint32_t rho0, uint8
     const int k = i & (kDim / 16 - 1);
     return (i < kDim / 16 ? q1 : q2) + (kDim == 128 ? row * 128 + ((k ^ (row & 7)) << 4) : row * 64 + ((k ^ ((row >> 1) & 3)) << 4));
   };
-#pragma unroll 1
+  const uint32_t group = static_cast<uint32_t>(p.group);
+  uint32_t i = (rho0 + sub) / group, g = rho0 + sub - i * group;  // query row and head within the kv head
+  const uint8_t* base = p.q + w.row0 * p.q_row + static_cast<int64_t>(w.h) * group * p.q_head + 16 * c;
+#pragma unroll 4
   for (int k = 0; k < 32 / kAtOnce; ++k) {
-    const int r = k * kAtOnce + sub;
-    const uint32_t rho = rho0 + r, i = rho / static_cast<uint32_t>(p.group);
-    const uint32_t head = w.h * p.group + (rho - i * p.group);
     const bool live = static_cast<int>(i) < w.nq;
-    const uint8_t* src = p.q + (live ? static_cast<int64_t>(w.row0 + i) * p.q_row + head * p.q_head + 16 * c : 0);
+    const uint8_t* src = live ? base + i * p.q_row + g * p.q_head : base;
     // a row that is not there: nothing is read and the place is filled with zeros
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(row0 + r, c))), "l"(src), "r"(live ? 16 : 0)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(row0 + k * kAtOnce + sub, c))),
+                 "l"(src), "r"(live ? 16 : 0)
                  : "memory");
+    for (g += kAtOnce; g >= group; g -= group) ++i;
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
@@ -682,8 +717,10 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     int key_first = 1, key_last = 0;  // the keys this thread's row sees
     auto begin_piece = [&](const Piece& w) {
       const Row o = row_of(p, w, row);
-      key_first = o.lo;
-      key_last = o.hi;
+      // a row that is not there (its query is 0, its result goes nowhere)
+      // counts as seeing everything, so that it asks for no masks
+      key_first = o.live ? o.lo : 0;
+      key_last = o.live ? o.hi : 0x7FFFFFF0;
       fac = prepare_q<kDim>(p, w, w.mt * kTilesM + gi * kGroupRows + quarter * 32, q1, q2, quarter * 32);
       fence_proxy_async();
       __syncwarp();
@@ -703,52 +740,56 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       if (!on) {
         T += tiles;
       } else {
-        for (int j = 0; j < tiles; ++j, ++T, ++used) {
+        // Tiles [full0, full1) are seen whole by every row of the warp.
+        int full0 = (key_first + kTilesN - 1) / kTilesN - tile0, full1 = (key_last + 1) / kTilesN - tile0;
+        if (key_last < key_first) full1 = -1;
+        full0 = __reduce_max_sync(0xffffffffu, full0);
+        full1 = __reduce_min_sync(0xffffffffu, full1);
+        wait(sh.s_full[gi][used & 1], (used >> 1) & 1);  // before scales: this warp may have skipped tiles
+        wait(sh.sc_full[T % kScaleSlots], (T / kScaleSlots) & 1);
+        float2 sc = sh.scale[T % kScaleSlots];
+        for (int j = 0; j < tiles; ++j) {
           const uint32_t t_p = t_s + 64 * (used & 1);
-          if (j == 0) wait(sh.s_full[gi][used & 1], (used >> 1) & 1);  // before scales: this warp may have skipped tiles
-          wait2(sh.s_full[gi][used & 1], (used >> 1) & 1, sh.sc_full[T % kScaleSlots], (T / kScaleSlots) & 1);
+          if (j > 0) wait(sh.s_full[gi][used & 1], (used >> 1) & 1);
           tc_fence_after();
-          const float2 sc = sh.scale[T % kScaleSlots];
-          const int key0 = (tile0 + j) * kTilesN;
-          float s[kTilesN];
-          {
-            uint32_t u[2][32];
-            tmem_ld32(t_p, u[0]);
-            tmem_ld32(t_p + 32, u[1]);
-            tmem_ld_wait(u[0]);
-            tmem_ld_wait(u[1]);
-#pragma unroll
-            for (int i = 0; i < kTilesN; ++i) s[i] = __uint_as_float(u[i / 32][i % 32]);
-          }
-          const bool all = key_first <= key0 && key_last >= key0 + kTilesN - 1 && sc.x > 0.f;
-          if (!__all_sync(0xffffffffu, all)) {
-            const int lo = key_first - key0, span = sc.x > 0.f ? key_last - key_first : -1;
+          uint32_t u[2][32];
+          tmem_ld32(t_p, u[0]);
+          tmem_ld_wait(u[0]);
+          tmem_ld32(t_p + 32, u[1]);
+          float top = max_of_32(u[0]);
+          tmem_ld_wait(u[1]);
+          if (j < full0 || j >= full1 || !(sc.x > 0.f)) {
+            const int lo = key_first - (tile0 + j) * kTilesN, span = sc.x > 0.f ? key_last - key_first : -1;
 #pragma unroll
             for (int i = 0; i < kTilesN; ++i) {
               const bool seen = span >= 0 && static_cast<uint32_t>(i - lo) <= static_cast<uint32_t>(span);
-              s[i] = seen ? s[i] : -INFINITY;
+              u[i / 32][i % 32] = seen ? u[i / 32][i % 32] : 0xFF800000u;
             }
+            top = max_of_32(u[0]);
           }
-          float c = fmaxf(fac * fabsf(sc.x), FLT_MIN);
-          // The weights take s c - m in one fused step, m being the rounded
-          // maximum: a difference that is off by up to 2^-24 |m|, the same for
-          // the whole row, and so of no effect until it nears the weights'
-          // headroom.  Logits that large are rounded first.
-          float top = __fmul_rn(max_of_64(s), c) + sc.y;
-          float lazy = kLazyLog2;
-          if (__any_sync(0xffffffffu, fabsf(top) > 4194304.f && top > -INFINITY)) {
+          top = fmaxf(top, max_of_32(u[1]));
+          float s[kTilesN];
 #pragma unroll
-            for (int i = 0; i < kTilesN; ++i) s[i] *= c;
-            c = 1.f;
-            lazy = 0.f;
-          }
-          const bool move = top > m + lazy;
-          if (__any_sync(0xffffffffu, move)) {
-            const float mn = move ? top : m;
+          for (int i = 0; i < kTilesN; ++i) s[i] = __uint_as_float(u[i / 32][i % 32]);
+          float c = fmaxf(fac * fabsf(sc.x), FLT_MIN);
+          top = __fmul_rn(top, c) + sc.y;
+          if (__any_sync(0xffffffffu, top > m + kLazyLog2 || fabsf(top) > kLargeLog2)) {
+            // The weights take s c - m in one fused step, m being the rounded
+            // maximum: a difference that is off by up to 2^-24 |m|, the same
+            // for the whole row, and so of no effect until it nears the
+            // weights' headroom.  Logits that large are rounded first, and the
+            // maximum then follows them closely.
+            const bool large = __any_sync(0xffffffffu, fabsf(top) > kLargeLog2 && top > -INFINITY);
+            if (large) {
+#pragma unroll
+              for (int i = 0; i < kTilesN; ++i) s[i] *= c;
+              c = 1.f;
+            }
+            const float mn = top > m + (large ? 0.f : kLazyLog2) ? top : m;
             const float shrink = exp2f(m - mn);
             m = mn;
             l *= shrink;
-            if (j > 0) {  // O holds the tiles before; their last product has to be done
+            if (j > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {  // O holds the tiles before; their last product has to be done
               wait(sh.o_done[gi], (used - 1) & 1);
               tc_fence_after();
 #pragma unroll 1
@@ -770,20 +811,32 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             float x, y;
-            unpack2(fma2(pack2(s[2 * i], s[2 * i + 1]), cc, bb), x, y);
-            x = exp2_fast(x);
-            y = exp2_fast(y);
+            const uint64_t v = fma2(pack2(s[2 * i], s[2 * i + 1]), cc, bb);
+            if ((i * kPolyPairs) / 32 != ((i + 1) * kPolyPairs) / 32) {
+              exp2_poly2(v, x, y);
+            } else {
+              unpack2(v, x, y);
+              x = exp2_fast(x);
+              y = exp2_fast(y);
+            }
             sum[i & 3] = add2(sum[i & 3], pack2(x, y));
             h[i] = pack_half2(x, y);
           }
           tmem_st32(t_p, h);
+          // while the weights are on their way: the row's sum, the next scales
+          float x, y;
+          unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
+          l += (x + y) * pow2i(-static_cast<int>(sc.y));
+          ++T;
+          if (j + 1 < tiles) {  // there long since
+            wait(sh.sc_full[T % kScaleSlots], (T / kScaleSlots) & 1);
+            sc = sh.scale[T % kScaleSlots];
+          }
           tmem_st_wait();
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&sh.p_full[gi][used & 1]));
-          float x, y;
-          unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
-          l += (x + y) * pow2i(-static_cast<int>(sc.y));
+          ++used;
         }
       }
       // the next piece's queries, so that its first product runs while this
@@ -798,13 +851,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       auto store_lse = [&](float top, float sum) {
         if (p.lse != nullptr && mine.live)
           p.lse[mine.token * (static_cast<int64_t>(p.kv_heads) * p.group) + mine.head] =
-              sum == 0.f ? -INFINITY : (top - kWeightLog2 + log2f(sum)) * kLn2;
+              saw_nothing(top, sum) ? -INFINITY : (top - kWeightLog2 + log2f(sum)) * kLn2;
       };
       uint8_t* dst = p.out + mine.token * p.out_row + mine.head * p.out_head;
       if (on) {
         wait(sh.o_done[gi], (used - 1) & 1);
         tc_fence_after();
-        const float inv = l == 0.f ? 0.f : 1.0f / l;
+        const float inv = saw_nothing(m, l) ? 0.f : 1.0f / l;
         float* part = p.part + slot * Cfg::kPartFloats;
 #pragma unroll 1
         for (int c = 0; c < kDim / 32; ++c) {
@@ -870,25 +923,40 @@ attention_join_kernel(const __grid_constant__ AttnParams p) {
   const Row o = row_of(p, w, row);
   if (!o.live) return;
   auto part_of = [&](int i) { return p.part + static_cast<size_t>(2 * (w.c0 + i) + (i == 0 ? 1 : 0)) * kPartFloats; };
-  float top = -FLT_MAX;
-#pragma unroll 4
-  for (int i = 0; i < w.parts; ++i) top = fmaxf(top, __ldcg(part_of(i) + kTilesM * kDim + row));
-  float sum = 0.f, x[16] = {};
-#pragma unroll 4
-  for (int i = 0; i < w.parts; ++i) {
-    const float* src = part_of(i);
-    const float f = join_weight(__ldcg(src + kTilesM * kDim + row), top);
-    sum += __ldcg(src + kTilesM * kDim + kTilesM + row) * f;
+  float top = -FLT_MAX, sum = 0.f, x[16] = {};
+  for (int i0 = 0; i0 < w.parts; i0 += 4) {  // every read of four parts before the first use
+    float m[4], l[4];
+    float4 v[4][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + (4 * c + k) * kTilesM + row);
-      x[4 * k] += v.x * f;
-      x[4 * k + 1] += v.y * f;
-      x[4 * k + 2] += v.z * f;
-      x[4 * k + 3] += v.w * f;
+    for (int i = 0; i < 4; ++i) {
+      const float* src = part_of(min(i0 + i, w.parts - 1));
+      m[i] = i0 + i < w.parts ? __ldcg(src + kTilesM * kDim + row) : -FLT_MAX;
+      l[i] = i0 + i < w.parts ? __ldcg(src + kTilesM * kDim + kTilesM + row) : 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        v[i][k] = i0 + i < w.parts ? __ldcg(reinterpret_cast<const float4*>(src) + (4 * c + k) * kTilesM + row)
+                                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const float now = fmaxf(fmaxf(top, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
+    const float old = join_weight(top, now);
+    top = now;
+    sum *= old;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] *= old;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float f = join_weight(m[i], top);
+      sum += l[i] * f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        x[4 * k] += v[i][k].x * f;
+        x[4 * k + 1] += v[i][k].y * f;
+        x[4 * k + 2] += v[i][k].z * f;
+        x[4 * k + 3] += v[i][k].w * f;
+      }
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.0f / sum;
+  const float inv = saw_nothing(top, sum) ? 0.f : 1.0f / sum;
   uint32_t b[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -900,7 +968,7 @@ attention_join_kernel(const __grid_constant__ AttnParams p) {
   dst[1] = make_uint4(b[4], b[5], b[6], b[7]);
   if (p.lse != nullptr && c == 0)
     p.lse[o.token * (static_cast<int64_t>(p.kv_heads) * p.group) + o.head] =
-        sum == 0.f ? -INFINITY : (top - kWeightLog2 + log2f(sum)) * kLn2;
+        saw_nothing(top, sum) ? -INFINITY : (top - kWeightLog2 + log2f(sum)) * kLn2;
 }
 
 template <int kDim>

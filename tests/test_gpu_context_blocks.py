@@ -78,7 +78,7 @@ def test_blocks_over_a_context():
         # code (at most 448) and page scale.  It shows here: in some columns every token with weight has
         # the value 0, and the others' sum is 1e-13.
         tail = 2.0 ** -35 * n * 448 * cache.v_scale[torch.from_numpy(page).long().cuda()].max().item()
-        tol = 2.0 ** -8 * np.abs(w[0]) + (2.0 ** -11 + 2.0 ** -20 + 2 * d) * mass[0] + tail
+        tol = 2.0 ** -8 * np.abs(w[0]) + (2.0 ** -11 + 2.0 ** -18 + 2 * d) * mass[0] + tail
         at = np.unravel_index(np.argmax(err / tol), err.shape)
         assert np.all(err <= tol), (j, k, at, err[at], tol[at], w[0][at], mass[0][at], size[0])
         calls.append((j, k))
