@@ -86,7 +86,10 @@ struct TilesShared {
   Piece piece[kPieceSlots];
   float2 scale[kScaleSlots];  // (k scale, value exponent) of the tile's page; k scale < 0: page not there
   uint64_t k_full[6], k_empty[6], v8_full[4], v8_empty[4], vh_full[4], vh_empty[4];
-  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2];  // [group], [group][S buffer]
+  // [group], [group][S buffer].  A wait names a phase by its parity, so a
+  // barrier must never be two phases from the one waited for: the last P V and
+  // the one before it may both be under way, hence one o_done per buffer.
+  uint64_t q_full[2], s_full[2][2], p_full[2][2], o_done[2][2];
   uint64_t sc_full[kScaleSlots], piece_full[kPieceSlots], piece_empty[kPieceSlots];
   uint32_t tmem;
 };
@@ -437,8 +440,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       for (int b = 0; b < 2; ++b) {
         mbar_init(smem_u32(&sh.s_full[s][b]), 1);
         mbar_init(smem_u32(&sh.p_full[s][b]), 4);
+        mbar_init(smem_u32(&sh.o_done[s][b]), 1);
       }
-      mbar_init(smem_u32(&sh.o_done[s]), 1);
     }
     for (int s = 0; s < kScaleSlots; ++s) mbar_init(smem_u32(&sh.sc_full[s]), 1);
     fence_mbarrier_init();
@@ -602,11 +605,11 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       auto score = [&](bool first) {
         // The buffer is free once P V of two tiles back is done.  A piece's
         // first S comes after the last P V before it, any other ahead of the P V
-        // in between; o_done is never more than one phase further.
+        // in between.
         if (on && first) wait(sh.q_full[gi], pieces & 1);
         const uint32_t behind = first ? b - 1 : a - 2;
         if (on && static_cast<int>(behind) >= 0)
-          wait2(sh.k_full[sk], pk, sh.o_done[gi], behind & 1);
+          wait2(sh.k_full[sk], pk, sh.o_done[gi][behind & 1], (behind >> 1) & 1);
         else
           wait(sh.k_full[sk], pk);
         if (!ok) return;
@@ -644,7 +647,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
           mma_f16_ts(t_o, s, vb, v_hi, idesc_o, j > 0);
 #pragma unroll
           for (int k = 1; k < kTilesN / 16; ++k) mma_f16_ts(t_o, s + 8 * k, vb + 128 * k, v_hi, idesc_o, 1u);
-          tc_commit1(smem_u32(&sh.o_done[gi]));
+          tc_commit1(smem_u32(&sh.o_done[gi][b & 1]));
           tc_commit1(smem_u32(&sh.vh_empty[sv]));
           ++b;
         } else {
@@ -660,7 +663,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     }
     // its products have completed before tensor memory is freed
     if (a > b) mbar_wait_bounded(smem_u32(&sh.s_full[gi][(a - 1) & 1]), ((a - 1) >> 1) & 1, p.wait_ns);
-    if (b > 0) mbar_wait_bounded(smem_u32(&sh.o_done[gi]), (b - 1) & 1, p.wait_ns);
+    if (b > 0) mbar_wait_bounded(smem_u32(&sh.o_done[gi][(b - 1) & 1]), ((b - 1) >> 1) & 1, p.wait_ns);
     __syncwarp();
   } else if (warp >= kConvWarp0) {
     // ---- V's codes to float16: half a key per thread; both layouts keep a key's
@@ -790,7 +793,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
             m = mn;
             l *= shrink;
             if (j > 0 && __any_sync(0xffffffffu, shrink != 1.f)) {  // O holds the tiles before; their last product has to be done
-              wait(sh.o_done[gi], (used - 1) & 1);
+              wait(sh.o_done[gi][(used - 1) & 1], ((used - 1) >> 1) & 1);
               tc_fence_after();
 #pragma unroll 1
               for (int c16 = 0; c16 < kDim / 16; ++c16) {
@@ -855,7 +858,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       };
       uint8_t* dst = p.out + mine.token * p.out_row + mine.head * p.out_head;
       if (on) {
-        wait(sh.o_done[gi], (used - 1) & 1);
+        wait(sh.o_done[gi][(used - 1) & 1], ((used - 1) >> 1) & 1);
         tc_fence_after();
         const float inv = saw_nothing(m, l) ? 0.f : 1.0f / l;
         float* part = p.part + slot * Cfg::kPartFloats;

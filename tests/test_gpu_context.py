@@ -589,3 +589,25 @@ def test_two_steps_of_generation_together():
     layer([256, 256], False, [1, 1])  # encoded
     layer([256, 256], True, [0, 0])   # the next block
     assert plan.lens.cpu().tolist() == [582, 517] and dg.context_status(plan) == 0
+
+
+def test_attention_under_load_equals_itself():
+    # a batch with several pieces of work per SM, many times over and from several streams: every
+    # result equals the first bit for bit, and the first the one computed request by request
+    rng = np.random.default_rng(16)
+    held = rng.integers(200, 1500, 12).tolist()
+    plan, cache, q = setup(rng, held, [256] * 12, 11, 1, 128)
+    first, _ = check_attention(plan, cache, q, None, rows_of=[0, 77, 255])
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    work = [(s, dg.ContextWorkspace(plan.rows, 11, 1, 128), torch.zeros_like(q)) for s in streams]
+    torch.cuda.synchronize()
+    for _ in range(40):
+        for s, ws, out in work:
+            dg.context_attention(plan, cache, q, out, ws, stream=s)
+        torch.cuda.synchronize()
+        for s, ws, out in work:
+            assert torch.equal(out, first)
+            out.zero_()
+        torch.cuda.synchronize()
+    for _, ws, _ in work:
+        assert dg.device_status(ws) == 0
