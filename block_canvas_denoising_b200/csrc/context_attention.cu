@@ -36,22 +36,28 @@ constexpr float kWeightLog2 = 10.f;  // weights are at most 2^10
 // ---------------------------------------------------------------------------
 // few rows: warps on their own, mma.sync over pages
 // ---------------------------------------------------------------------------
-constexpr int kRowsM = 16;
-constexpr int kRowsWarps = 4;
-constexpr int kRowsThreads = kRowsWarps * 32;
-
-template <int kDim>
+// kNt: the rows of an item, in eights.
+template <int kDim, int kNt>
 struct RowsCfg {
+  static constexpr int kM = 8 * kNt;
+  // Warps of a block.  What bounds it is registers (97 to 160 a thread) and
+  // the warps' pages in shared memory.
+  static constexpr int kWarps = kNt == 1 ? (kDim == 128 ? 12 : 16) : 8;
+  static constexpr int kThreads = 32 * kWarps;
   static constexpr int kPageBytes = DG_PAGE * kDim;             // codes of one (page, head), k or v
-  static constexpr int kStages = kDim == 128 ? 3 : 6;           // pages in flight per warp
-  static constexpr int kRing = kRowsWarps * kStages * 2 * kPageBytes;
-  static constexpr int kSmem = kRing + 1024 + 1024;
-  static constexpr int kPartFloats = kRowsM * (kDim + 2);
+  // A page of keys and one of values per warp.  The next keys are asked for
+  // as soon as these are multiplied, the next values likewise, so one of the
+  // two is always on its way: 64 KB or more in flight on an SM.
+  static constexpr int kRing = kWarps * 2 * kPageBytes;
+  static constexpr int kSmem = kRing + 1024;
+  static constexpr int kPartFloats = kM * (kDim + 2);
+  static_assert(kRing >= kWarps * kM * kDim * 4 && kSmem <= 220 * 1024, "the warps meet in the ring");
 };
 
+// Not volatile, like the conversions: the compiler is free to put independent
+// products between dependent ones.
 DG_DEV void mma_16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
       "{%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -63,63 +69,52 @@ DG_DEV void codes_to_half(uint32_t w, uint32_t& lo, uint32_t& hi) {
       : "=r"(lo), "=r"(hi)
       : "r"(w));
 }
-DG_DEV uint4 lds128(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
-}
-DG_DEV uint2 lds64(uint32_t addr) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
-  return v;
-}
 DG_DEV uint32_t half2_of(float lo, float hi) {
   const __half2 h = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-
-// The power of two f (as its exponent) that brings a row's largest magnitude
-// to [2^14, 2^15): bf16 values times f are exact in float16 down to 2^-28 of
-// the largest, far below float32 sums of the products.  Returns false for a
-// row that holds a value that is not finite.
-DG_DEV bool row_exponent(float top, int& e) {
-  const int b = static_cast<int>(__float_as_uint(top) >> 23);
-  e = b == 0 ? 0 : min(14 - (b - 127), 120);
-  return b < 255;
+// The transpose of an 8 x 8 matrix of 16-bit elements, two per thread.
+DG_DEV uint32_t transpose8(uint32_t v) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(v));
+  return d;
 }
+
 // One warp walks its own pages with its own copies in flight and its own
-// softmax; the block's four warps meet once per item.  A page (64 keys) is 8
-// key tiles of mma.m16n8k16.  Which element of a head is "k index 2t" of an
-// instruction is free as long as both operands agree, and so is which key is
-// "k index" of the second product: thread t of a quad takes 32 consecutive
-// elements (16 at dim 64) of a key, so its operands are whole 16-byte reads
-// of the codes as the cache holds them, and the second product takes the
-// keys where the first left its results.  Nothing is transposed.
-template <int kDim>
-__global__ void __launch_bounds__(kRowsThreads, 1)
+// softmax; the block's warps meet once per item.  A page (64 keys) is four key
+// tiles of mma.m16n8k16 with the keys as the 16 rows and the item's rows as
+// the 8 columns: S^T = K Q^T and O^T = V^T P^T, so that no more than 8 of
+// those are paid for where there are 4 (with the rows as the 16: twice the
+// products and accumulators, 8 warps on an SM, and 2.4 TB/s of cache).
+// Which element of a head is "k index 2t" of an instruction is free as long
+// as both operands agree, and so is which element is which row of O^T: thread
+// t of a quad takes dim / 4 consecutive elements of a key, and quad g dim / 8
+// of a value, so operands are whole 16-byte reads of the codes as the cache
+// holds them.  Between the products P is transposed 8 x 8 at a time.
+template <int kDim, int kNt>
+__global__ void __launch_bounds__(RowsCfg<kDim, kNt>::kThreads, 1)
 attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                       const __grid_constant__ AttnParams p) {
-  using Cfg = RowsCfg<kDim>;
-  using S = Split<kRowsM, DG_PAGE>;
+  using Cfg = RowsCfg<kDim, kNt>;
+  using S = Split<Cfg::kM, DG_PAGE, 2 * Cfg::kWarps>;  // an item costs about two pages a warp
+  constexpr int kM = Cfg::kM, kWarps = Cfg::kWarps;
   constexpr int kSteps = kDim / 16;      // k steps of q . k
-  constexpr int kNt = kDim / 8;          // 8-wide output tiles
   constexpr int kSlice = kDim / 4;       // elements of a key held by one thread of a quad
+  constexpr int kDt = kDim / 16;         // 16-row tiles of O^T
+  constexpr int kVw = kDim / 32;         // words of a value held by a thread
   extern __shared__ uint8_t smem_raw[];
   __shared__ int64_t s_before[DG_MAX_B + 1];
-  __shared__ uint64_t s_bars[kRowsWarps][Cfg::kStages][2];
-  __shared__ float s_scale[kRowsWarps][Cfg::kStages][2];
-  __shared__ float s_m[kRowsWarps][kRowsM], s_l[kRowsWarps][kRowsM];
+  __shared__ uint64_t s_bars[kWarps][2];
+  __shared__ float s_m[kWarps][kM], s_l[kWarps][kM];
   __shared__ uint32_t s_last;
   uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* s_o = reinterpret_cast<float*>(ring);  // [warps][16][dim], between items
+  float* s_o = reinterpret_cast<float*>(ring);  // [warps][kM][dim], between items
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, t = lane & 3;
 
   if (lane == 0) {
-    for (int s = 0; s < Cfg::kStages; ++s) {
-      mbar_init(smem_u32(&s_bars[warp][s][0]), 1);
-      mbar_init(smem_u32(&s_bars[warp][s][1]), 1);
-    }
+    mbar_init(smem_u32(&s_bars[warp][0]), 1);
+    mbar_init(smem_u32(&s_bars[warp][1]), 1);
     fence_mbarrier_init();
   }
   S::totals(p, s_before);
@@ -129,74 +124,73 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
   int64_t pos = blockIdx.x * per;
   const int64_t end = min(pos + per, total);
   const uint64_t policy = policy_evict_first();
-  int stage = 0;
+  uint8_t* k_page = ring + warp * 2 * Cfg::kPageBytes;
+  uint8_t* v_page = k_page + Cfg::kPageBytes;
+  const uint32_t k_bar = smem_u32(&s_bars[warp][0]), v_bar = smem_u32(&s_bars[warp][1]);
   uint32_t phase = 0;
   bool ok = true;
 
   while (pos < end) {
     S it;
     it.find(p, s_before, pos);
+    pos = max(pos, it.begin);  // the units before an item's first tile stand for its fixed cost
+    if (pos >= end) break;
     const int64_t item_end = it.begin + it.tiles;
     const int seg = static_cast<int>(min(item_end, end) - pos);
     const int page0 = it.first + static_cast<int>(pos - it.begin);
     const Request& rq = it.q;
-    const int mine = seg > warp ? (seg - warp + kRowsWarps - 1) / kRowsWarps : 0;
+    const int mine = seg > warp ? (seg - warp + kWarps - 1) / kWarps : 0;
 
-    // copies: lane l of the warp knows the id and scales of its pages 32 j + l
+    // ids and scales of the warp's pages n0 .. n0 + 31, one per lane
     int id = 0;
     float ks = 1.f, vs = 1.f;
-    auto issue = [&](int n) {
-      if ((n & 31) == 0) {
-        const int m = n + lane;
-        const int pg = page0 + warp + m * kRowsWarps;
-        id = -1;
-        if (m < mine && pg < p.max_pages) id = p.table[static_cast<size_t>(it.r) * p.max_pages + pg];
-        ks = vs = 1.f;
-        if (id < 0 || id >= p.pages) {
-          id = p.pages;  // outside the tensor: the copy fills zeros
-          ks = -1.f;     // and its keys are not seen
-        } else {
-          ks = p.k_scale[static_cast<size_t>(id) * p.kv_heads + it.h];
-          vs = p.v_scale[static_cast<size_t>(id) * p.kv_heads + it.h];
-        }
-      }
-      const int n_id = __shfl_sync(0xffffffffu, id, n & 31);
-      const float n_ks = __shfl_sync(0xffffffffu, ks, n & 31), n_vs = __shfl_sync(0xffffffffu, vs, n & 31);
-      int st = stage + (n < Cfg::kStages ? n : 0);  // ahead of the reader only before the loop
-      if (st >= Cfg::kStages) st -= Cfg::kStages;
-      if (lane == 0) {
-        s_scale[warp][st][0] = n_ks;
-        s_scale[warp][st][1] = n_vs;
-        const int y = (n_id * p.kv_heads + it.h) * DG_PAGE;
-        const uint32_t dst = smem_u32(ring) + ((warp * Cfg::kStages + st) * 2) * Cfg::kPageBytes;
-        const uint32_t kb = smem_u32(&s_bars[warp][st][0]), vb = smem_u32(&s_bars[warp][st][1]);
-        mbar_arrive_expect_tx(kb, Cfg::kPageBytes);
-        tma_load_2d(dst, &tmK, kb, 0, y, policy);
-        mbar_arrive_expect_tx(vb, Cfg::kPageBytes);
-        tma_load_2d(dst + Cfg::kPageBytes, &tmV, vb, 0, y, policy);
+    auto look_up = [&](int n0) {
+      const int n = n0 + lane, pg = page0 + warp + n * kWarps;
+      id = -1;
+      if (n < mine && pg < p.max_pages) id = p.table[static_cast<size_t>(it.r) * p.max_pages + pg];
+      if (id < 0 || id >= p.pages) {
+        id = p.pages;  // outside the tensor: the copy fills zeros
+        ks = -1.f;     // and its keys are not seen
+        vs = 1.f;
+      } else {
+        ks = p.k_scale[static_cast<size_t>(id) * p.kv_heads + it.h];
+        vs = p.v_scale[static_cast<size_t>(id) * p.kv_heads + it.h];
       }
     };
-    for (int n = 0; n < Cfg::kStages && n < mine; ++n) issue(n);
+    // all lanes; only page n of the looked up ones
+    auto copy = [&](const CUtensorMap* map, uint8_t* to, uint32_t bar, int n) {
+      const int y = (__shfl_sync(0xffffffffu, id, n & 31) * p.kv_heads + it.h) * DG_PAGE;
+      if (lane == 0) {
+        mbar_arrive_expect_tx(bar, Cfg::kPageBytes);
+        tma_load_2d(smem_u32(to), map, bar, 0, y, policy);
+      }
+    };
+    if (mine > 0) {
+      look_up(0);
+      copy(&tmK, k_page, k_bar, 0);
+      copy(&tmV, v_page, v_bar, 0);
+    }
 
-    // this thread's rows g and g + 8 of the item: operands and factor
-    uint32_t qf[kSteps][4];
-    float fac[2];
-    int lo[2], hi[2];
+    // queries: thread (g, t) holds its slice of rows g (and g + 8) as operands;
+    // thread t is in charge of the softmax of rows 2t, 2t + 1 (and 8 further)
+    uint32_t qf[kNt][kSteps][2];
+    float fac[kNt][2];
+    int lo[kNt][2], hi[kNt][2];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int64_t rho = static_cast<int64_t>(it.mt) * kRowsM + g + 8 * half;
-      const int i = static_cast<int>(rho / p.group), head = it.h * p.group + static_cast<int>(rho % p.group);
+    for (int nt = 0; nt < kNt; ++nt) {
+      const uint32_t rho = static_cast<uint32_t>(it.mt) * kM + 8 * nt + g;
+      const int i = static_cast<int>(rho / static_cast<uint32_t>(p.group));
+      const int head = it.h * p.group + static_cast<int>(rho - static_cast<uint32_t>(i) * p.group);
       const bool live = i < rq.nq;
-      lo[half] = live ? key_lo(p, rq, i) : 1;
-      hi[half] = live ? key_hi(rq, i) : 0;
       float x[kSlice];
       float top = 0.f;
-      bool finite = true;
+      int fin = 1;
 #pragma unroll
       for (int c = 0; c < kSlice / 8; ++c) {
         uint4 w = make_uint4(0, 0, 0, 0);
         if (live)
-          w = *reinterpret_cast<const uint4*>(p.q + (rq.row0 + i) * p.q_row + head * p.q_head + 2 * kSlice * t + 16 * c);
+          w = *reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(rq.row0 + i) * p.q_row + head * p.q_head +
+                                              2 * kSlice * t + 16 * c);
         const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -206,180 +200,236 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float a = fabsf(x[8 * c + j]);
-          finite = finite && a <= FLT_MAX;
+          fin &= a <= FLT_MAX;
           top = fmaxf(top, a);
         }
       }
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      int fin = finite;
-      fin &= __shfl_xor_sync(0xffffffffu, fin, 1);
-      fin &= __shfl_xor_sync(0xffffffffu, fin, 2);
-      int e;
-      row_exponent(top, e);
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        fin &= __shfl_xor_sync(0xffffffffu, fin, d);
+      }
+      // The power of two that brings the row's largest magnitude to [2^14,
+      // 2^15): bf16 values times it are exact in float16 down to 2^-28 of the
+      // largest, far below the float32 sums of the products.
+      const int b = static_cast<int>(__float_as_uint(top) >> 23);
+      const int e = b == 0 ? 0 : min(14 - (b - 127), 120);
       const float f = fin ? pow2i(e) : 0.f;
-      fac[half] = fin ? p.scale_log2 * pow2i(-e) : __int_as_float(0x7fc00000);
 #pragma unroll
       for (int s = 0; s < kSteps; ++s) {
-        qf[s][half] = half2_of(x[4 * s] * f, x[4 * s + 1] * f);
-        qf[s][2 + half] = half2_of(x[4 * s + 2] * f, x[4 * s + 3] * f);
+        qf[nt][s][0] = half2_of(x[4 * s] * f, x[4 * s + 1] * f);
+        qf[nt][s][1] = half2_of(x[4 * s + 2] * f, x[4 * s + 3] * f);
+      }
+      // a row that holds a value that is not finite: NaN for all its logits
+      const float mine_fac = fin ? p.scale_log2 * pow2i(-e) : __int_as_float(0x7fc00000);
+      const int my_lo = live ? key_lo(p, rq, i) : 0, my_hi = live ? key_hi(rq, i) : 0x7FFFFFF0;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        fac[nt][k] = __shfl_sync(0xffffffffu, mine_fac, 4 * (2 * t + k));
+        lo[nt][k] = __shfl_sync(0xffffffffu, my_lo, 4 * (2 * t + k));
+        hi[nt][k] = __shfl_sync(0xffffffffu, my_hi, 4 * (2 * t + k));
       }
     }
 
-    float m[2] = {-FLT_MAX, -FLT_MAX}, l[2] = {0.f, 0.f};
-    float o[kNt][4];
+    float m[kNt][2], l[kNt][2], o[kNt][kDt][4];
 #pragma unroll
-    for (int j = 0; j < kNt; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.f;
+    for (int nt = 0; nt < kNt; ++nt) {
+      m[nt][0] = m[nt][1] = -FLT_MAX;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int d = 0; d < kDt; ++d) o[nt][d][0] = o[nt][d][1] = o[nt][d][2] = o[nt][d][3] = 0.f;
+    }
 
     for (int n = 0; n < mine; ++n) {
-      __syncwarp();
-      const float ks_n = s_scale[warp][stage][0], vs_n = s_scale[warp][stage][1];
-      const uint32_t kbase = smem_u32(ring) + ((warp * Cfg::kStages + stage) * 2) * Cfg::kPageBytes;
-      const uint32_t vbase = kbase + Cfg::kPageBytes;
-      const int key0 = (page0 + warp + n * kRowsWarps) * DG_PAGE;
-      if (ok && !mbar_wait_bounded(smem_u32(&s_bars[warp][stage][0]), phase, p.wait_ns)) ok = false;
-      float s[8][4];
+      const float ks_n = __shfl_sync(0xffffffffu, ks, n & 31), vs_n = __shfl_sync(0xffffffffu, vs, n & 31);
+      const int key0 = (page0 + warp + n * kWarps) * DG_PAGE;
+      const bool more = n + 1 < mine;
+      if (ok && !mbar_wait_bounded(k_bar, phase, p.wait_ns)) ok = false;
+      // S^T: s[nt][i] = keys 16 i + g (elements 0, 1: rows 2t, 2t + 1) and 16 i + g + 8 (2, 3)
+      float s[kNt][4][4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
-        uint32_t w[kSlice / 4];
-        const int row = 8 * j + g;
-        if (kDim == 128) {  // chunks 2t, 2t + 1 of a 128-byte row, swizzled by the row
+      for (int i = 0; i < 4; ++i) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            const uint4 v = lds128(kbase + row * 128 + (((2 * t + c) ^ (row & 7)) << 4));
-            w[4 * c] = v.x; w[4 * c + 1] = v.y; w[4 * c + 2] = v.z; w[4 * c + 3] = v.w;
+        for (int nt = 0; nt < kNt; ++nt) s[nt][i][0] = s[nt][i][1] = s[nt][i][2] = s[nt][i][3] = 0.f;
+        uint32_t w[2][kSlice / 4];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const int row = 16 * i + 8 * k + g;
+#pragma unroll
+          for (int c = 0; c < kSlice / 16; ++c) {
+            // dim 128: chunks 2t, 2t + 1 of a 128-byte row, swizzled by the row;
+            // dim 64: chunk t of a 64-byte row, swizzled by the row pair
+            const uint4 v = *reinterpret_cast<const uint4*>(
+                k_page + (kDim == 128 ? row * 128 + (((2 * t + c) ^ (row & 7)) << 4) : row * 64 + ((t ^ ((row >> 1) & 3)) << 4)));
+            w[k][4 * c] = v.x; w[k][4 * c + 1] = v.y; w[k][4 * c + 2] = v.z; w[k][4 * c + 3] = v.w;
           }
-        } else {  // chunk t of a 64-byte row, swizzled by the row pair
-          const uint4 v = lds128(kbase + row * 64 + ((t ^ ((row >> 1) & 3)) << 4));
-          w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
         }
 #pragma unroll
         for (int k = 0; k < kSteps; ++k) {
-          uint32_t b0, b1;
-          codes_to_half(w[k], b0, b1);
-          mma_16816(s[j], qf[k], b0, b1);
+          uint32_t a[4];
+          codes_to_half(w[0][k], a[0], a[2]);
+          codes_to_half(w[1][k], a[1], a[3]);
+#pragma unroll
+          for (int nt = 0; nt < kNt; ++nt) mma_16816(s[nt][i], a, qf[nt][k][0], qf[nt][k][1]);
         }
       }
+      __syncwarp();
+      const bool turn = more && ((n + 1) & 31) == 0;  // the next page is of the next 32
+      if (more && !turn) copy(&tmK, k_page, k_bar, n + 1);
       // logits, weights
       const bool seen = ks_n > 0.f;
-      const float e = seen ? static_cast<float>(static_cast<int>(__float_as_uint(vs_n) >> 23) - 127) : 0.f;
-      const float inv_vs = seen ? 1.0f / vs_n : 1.f;
+      const float ve = seen ? static_cast<float>(static_cast<int>(__float_as_uint(vs_n) >> 23) - 127) : 0.f;
+      bool all = seen;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const float c = fac[half] * ks_n;
-        float top = -INFINITY;
-        const bool all = seen && lo[half] <= key0 && hi[half] >= key0 + DG_PAGE - 1;
+      for (int nt = 0; nt < kNt; ++nt) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int k = 0; k < 2; ++k) all = all && lo[nt][k] <= key0 && hi[nt][k] >= key0 + DG_PAGE - 1;
+      }
+      all = __all_sync(0xffffffffu, all);
+      uint32_t pt[kNt][8];  // P^T as the second product's operand: keys 8 j + 2t, + 1 of row g
+      bool moved = false;
+      float shrink[kNt][2];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            float x = s[j][2 * half + k] * c;
-            const int key = key0 + 8 * j + 2 * t + k;
-            if (!all && (!seen || key < lo[half] || key > hi[half])) x = -INFINITY;
-            s[j][2 * half + k] = x;
-            top = fmaxf(top, x);
+      for (int nt = 0; nt < kNt; ++nt) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float c = fac[nt][k] * ks_n;
+          float top = -INFINITY;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              float x = s[nt][i][2 * h + k] * c;
+              if (!all) {
+                const int key = key0 + 16 * i + 8 * h + g;
+                if (!seen || key < lo[nt][k] || key > hi[nt][k]) x = -INFINITY;
+              }
+              s[nt][i][2 * h + k] = x;
+              top = fmaxf(top, x);
+            }
           }
-        }
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const float mn = fmaxf(m[half], top + e);
-        const float shrink = exp2f(m[half] - mn);
-        m[half] = mn;
-        const float off = e - mn + kWeightLog2;
-        float sum = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+          for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+          const float mn = fmaxf(m[nt][k], top + ve);
+          shrink[nt][k] = exp2f(m[nt][k] - mn);
+          moved = moved || mn != m[nt][k];
+          m[nt][k] = mn;
+          const float off = ve - mn + kWeightLog2;
+          float sum = 0.f;
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const float w = exp2_fast(s[j][2 * half + k] + off);
-            s[j][2 * half + k] = w;
-            sum += w;
+          for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float w = exp2_fast(s[nt][i][2 * h + k] + off);
+              s[nt][i][2 * h + k] = w;
+              sum += w;
+            }
           }
+          l[nt][k] = l[nt][k] * shrink[nt][k] + sum * pow2i(-static_cast<int>(ve));
         }
-        l[half] = l[half] * shrink + sum * inv_vs;
 #pragma unroll
-        for (int j = 0; j < kNt; ++j) {
-          o[j][2 * half] *= shrink;
-          o[j][2 * half + 1] *= shrink;
+        for (int i = 0; i < 4; ++i) {
+          pt[nt][2 * i] = transpose8(half2_of(s[nt][i][0], s[nt][i][1]));
+          pt[nt][2 * i + 1] = transpose8(half2_of(s[nt][i][2], s[nt][i][3]));
         }
       }
-      if (ok && !mbar_wait_bounded(smem_u32(&s_bars[warp][stage][1]), phase, p.wait_ns)) ok = false;
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int nt = 0; nt < kNt; ++nt) {
+#pragma unroll
+          for (int d = 0; d < kDt; ++d) {
+            o[nt][d][0] *= shrink[nt][0];
+            o[nt][d][1] *= shrink[nt][1];
+            o[nt][d][2] *= shrink[nt][0];
+            o[nt][d][3] *= shrink[nt][1];
+          }
+        }
+      }
+      if (ok && !mbar_wait_bounded(v_bar, phase, p.wait_ns)) ok = false;
       const int there = rq.len - key0;  // tokens of this page that exist
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint32_t a[4];
-        a[0] = half2_of(s[2 * i][0], s[2 * i][1]);
-        a[1] = half2_of(s[2 * i][2], s[2 * i][3]);
-        a[2] = half2_of(s[2 * i + 1][0], s[2 * i + 1][1]);
-        a[3] = half2_of(s[2 * i + 1][2], s[2 * i + 1][3]);
-        uint32_t w[4][kDim / 32];  // keys 2t, 2t + 1, 2t + 8, 2t + 9 of 16: dim / 8 elements each
+        uint32_t w[4][kVw];  // keys 2t, 2t + 1, 2t + 8, 2t + 9 of 16: dim / 8 elements each
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int row = 16 * i + 2 * t + (k & 1) + 8 * (k >> 1);
           if (kDim == 128) {
-            const uint4 v = lds128(vbase + row * 128 + ((g ^ (row & 7)) << 4));
-            w[k][0] = v.x; w[k][1] = v.y; w[k][kDim / 32 - 2] = v.z; w[k][kDim / 32 - 1] = v.w;
+            const uint4 v = *reinterpret_cast<const uint4*>(v_page + row * 128 + ((g ^ (row & 7)) << 4));
+            w[k][0] = v.x; w[k][1] = v.y; w[k][kVw - 2] = v.z; w[k][kVw - 1] = v.w;
           } else {
-            const uint2 v = lds64(vbase + row * 64 + ((((g >> 1) ^ ((row >> 1) & 3)) << 4) | ((g & 1) << 3)));
+            const uint2 v = *reinterpret_cast<const uint2*>(
+                v_page + row * 64 + ((((g >> 1) ^ ((row >> 1) & 3)) << 4) | ((g & 1) << 3)));
             w[k][0] = v.x; w[k][1] = v.y;
           }
-          if (row >= there) {
+        }
+        if (there < DG_PAGE) {  // behind the last token: zeros, whatever is there
 #pragma unroll
-            for (int j = 0; j < kDim / 32; ++j) w[k][j] = 0;
+          for (int k = 0; k < 4; ++k) {
+            if (16 * i + 2 * t + (k & 1) + 8 * (k >> 1) >= there) {
+#pragma unroll
+              for (int j = 0; j < kVw; ++j) w[k][j] = 0;
+            }
           }
         }
 #pragma unroll
-        for (int j = 0; j < kDim / 32; ++j) {
-          // bytes (key 2t, key 2t + 1) of each of 4 elements
-          uint32_t b[4][2];
-          codes_to_half(__byte_perm(w[0][j], w[1][j], 0x5140), b[0][0], b[1][0]);
-          codes_to_half(__byte_perm(w[0][j], w[1][j], 0x7362), b[2][0], b[3][0]);
-          codes_to_half(__byte_perm(w[2][j], w[3][j], 0x5140), b[0][1], b[1][1]);
-          codes_to_half(__byte_perm(w[2][j], w[3][j], 0x7362), b[2][1], b[3][1]);
+        for (int j = 0; j < kVw; ++j) {
+          // rows g and g + 8 of tile d are elements 2d and 2d + 1 of the quad's dim / 8
+          uint32_t a[2][4];
+          codes_to_half(__byte_perm(w[0][j], w[1][j], 0x5140), a[0][0], a[0][1]);
+          codes_to_half(__byte_perm(w[0][j], w[1][j], 0x7362), a[1][0], a[1][1]);
+          codes_to_half(__byte_perm(w[2][j], w[3][j], 0x5140), a[0][2], a[0][3]);
+          codes_to_half(__byte_perm(w[2][j], w[3][j], 0x7362), a[1][2], a[1][3]);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_16816(o[4 * j + k], a, b[k][0], b[k][1]);
+          for (int k = 0; k < 2; ++k) {
+#pragma unroll
+            for (int nt = 0; nt < kNt; ++nt) mma_16816(o[nt][2 * j + k], a[k], pt[nt][2 * i], pt[nt][2 * i + 1]);
+          }
         }
       }
       __syncwarp();
-      if (n + Cfg::kStages < mine) issue(n + Cfg::kStages);
-      if (++stage == Cfg::kStages) {
-        stage = 0;
-        phase ^= 1u;
+      if (turn) {
+        look_up(n + 1);
+        copy(&tmK, k_page, k_bar, n + 1);
       }
+      if (more) copy(&tmV, v_page, v_bar, n + 1);
+      phase ^= 1u;
     }
 
     // the warps meet: (m, l, o) of each through shared memory (the ring is
     // idle: every copy issued for this item has been waited for)
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
-      l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+    for (int nt = 0; nt < kNt; ++nt) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l[nt][k] += __shfl_xor_sync(0xffffffffu, l[nt][k], d);
+      }
     }
     __syncthreads();
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      const int row = g + 8 * half;
-      float* dst = s_o + (warp * kRowsM + row) * kDim + kSlice * t;
+    for (int nt = 0; nt < kNt; ++nt) {
 #pragma unroll
-      for (int j = 0; j < kNt; ++j) {  // columns 2t, 2t + 1 of tile j are elements slice + j, slice + dim / 8 + j
-        dst[j] = o[j][2 * half];
-        dst[kNt + j] = o[j][2 * half + 1];
-      }
-      if (t == 0) {
-        s_m[warp][row] = m[half];
-        s_l[warp][row] = l[half];
+      for (int k = 0; k < 2; ++k) {
+        const int row = 8 * nt + 2 * t + k;
+        float* dst = s_o + (warp * kM + row) * kDim + 2 * kDt * g;
+#pragma unroll
+        for (int d = 0; d < kDt; ++d) *reinterpret_cast<float2*>(dst + 2 * d) = make_float2(o[nt][d][k], o[nt][d][2 + k]);
+        if (g == 0) {
+          s_m[warp][row] = m[nt][k];
+          s_l[warp][row] = l[nt][k];
+        }
       }
     }
     __syncthreads();
 
-    const bool whole = it.begin >= blockIdx.x * per && item_end <= end;
+    const bool whole = pos == it.begin && item_end <= end;
     const int c0 = static_cast<int>(it.begin / per), parts = static_cast<int>((item_end - 1) / per) - c0 + 1;
     float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * Cfg::kPartFloats;
-    constexpr int kChunks = kRowsM * kDim / 8;
+    constexpr int kChunks = kM * kDim / 8;
     auto store = [&](int row, int d0, const float (&x)[8], float top, float sum) {
-      const int64_t rho = static_cast<int64_t>(it.mt) * kRowsM + row;
-      const int i = static_cast<int>(rho / p.group), head = it.h * p.group + static_cast<int>(rho % p.group);
+      const uint32_t rho = static_cast<uint32_t>(it.mt) * kM + row;
+      const int i = static_cast<int>(rho / static_cast<uint32_t>(p.group));
+      const int head = it.h * p.group + static_cast<int>(rho - static_cast<uint32_t>(i) * p.group);
       if (i >= rq.nq) return;
       const float inv = sum == 0.f ? 0.f : 1.0f / sum;
       uint32_t u[4];
@@ -388,24 +438,24 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * j] * inv, x[2 * j + 1] * inv);
         u[j] = *reinterpret_cast<const uint32_t*>(&b);
       }
-      *reinterpret_cast<uint4*>(p.out + (rq.row0 + i) * p.out_row + head * p.out_head + 2 * d0) =
+      *reinterpret_cast<uint4*>(p.out + static_cast<int64_t>(rq.row0 + i) * p.out_row + head * p.out_head + 2 * d0) =
           make_uint4(u[0], u[1], u[2], u[3]);
       if (p.lse != nullptr && d0 == 0)
         p.lse[static_cast<size_t>(rq.row0 + i) * (p.kv_heads * p.group) + head] =
             sum == 0.f ? -INFINITY : (top - kWeightLog2 + log2f(sum)) * kLn2;
     };
-    for (int c = threadIdx.x; c < kChunks; c += kRowsThreads) {
+    for (int c = threadIdx.x; c < kChunks; c += Cfg::kThreads) {
       const int row = c / (kDim / 8), d0 = (c % (kDim / 8)) * 8;
       float top = s_m[0][row];
 #pragma unroll
-      for (int w = 1; w < kRowsWarps; ++w) top = fmaxf(top, s_m[w][row]);
+      for (int w = 1; w < kWarps; ++w) top = fmaxf(top, s_m[w][row]);
       float sum = 0.f, x[8] = {};
 #pragma unroll
-      for (int w = 0; w < kRowsWarps; ++w) {
+      for (int w = 0; w < kWarps; ++w) {
         const float f = join_weight(s_m[w][row], top);
         sum += s_l[w][row] * f;
-        const float4 a = *reinterpret_cast<const float4*>(s_o + (w * kRowsM + row) * kDim + d0);
-        const float4 b = *reinterpret_cast<const float4*>(s_o + (w * kRowsM + row) * kDim + d0 + 4);
+        const float4 a = *reinterpret_cast<const float4*>(s_o + (w * kM + row) * kDim + d0);
+        const float4 b = *reinterpret_cast<const float4*>(s_o + (w * kM + row) * kDim + d0 + 4);
         x[0] += a.x * f; x[1] += a.y * f; x[2] += a.z * f; x[3] += a.w * f;
         x[4] += b.x * f; x[5] += b.y * f; x[6] += b.z * f; x[7] += b.w * f;
       }
@@ -416,8 +466,8 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         dst[0] = make_float4(x[0], x[1], x[2], x[3]);
         dst[1] = make_float4(x[4], x[5], x[6], x[7]);
         if (d0 == 0) {
-          part[kRowsM * kDim + row] = top;
-          part[kRowsM * kDim + kRowsM + row] = sum;
+          part[kM * kDim + row] = top;
+          part[kM * kDim + kM + row] = sum;
         }
       }
     }
@@ -436,19 +486,32 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         auto part_of = [&](int i) {
           return p.part + static_cast<size_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * Cfg::kPartFloats;
         };
-        for (int c = threadIdx.x; c < kChunks; c += kRowsThreads) {
+        for (int c = threadIdx.x; c < kChunks; c += Cfg::kThreads) {
           const int row = c / (kDim / 8), d0 = (c % (kDim / 8)) * 8;
-          float top = -FLT_MAX;
-          for (int i = 0; i < parts; ++i) top = fmaxf(top, __ldcg(part_of(i) + kRowsM * kDim + row));
-          float sum = 0.f, x[8] = {};
-          for (int i = 0; i < parts; ++i) {
-            const float* src = part_of(i);
-            const float f = join_weight(__ldcg(src + kRowsM * kDim + row), top);
-            sum += __ldcg(src + kRowsM * kDim + kRowsM + row) * f;
-            const float4 a = __ldcg(reinterpret_cast<const float4*>(src + row * kDim + d0));
-            const float4 b = __ldcg(reinterpret_cast<const float4*>(src + row * kDim + d0 + 4));
-            x[0] += a.x * f; x[1] += a.y * f; x[2] += a.z * f; x[3] += a.w * f;
-            x[4] += b.x * f; x[5] += b.y * f; x[6] += b.z * f; x[7] += b.w * f;
+          float top = -FLT_MAX, sum = 0.f, x[8] = {};
+          for (int i0 = 0; i0 < parts; i0 += 4) {  // every read of four parts before the first use
+            float m4[4], l4[4];
+            float4 a4[4], b4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float* src = part_of(min(i0 + i, parts - 1));
+              m4[i] = __ldcg(src + kM * kDim + row);
+              l4[i] = __ldcg(src + kM * kDim + kM + row);
+              a4[i] = __ldcg(reinterpret_cast<const float4*>(src + row * kDim + d0));
+              b4[i] = __ldcg(reinterpret_cast<const float4*>(src + row * kDim + d0 + 4));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i0 + i >= parts) break;
+              const float now = fmaxf(top, m4[i]);
+              const float old = join_weight(top, now), f = join_weight(m4[i], now);
+              top = now;
+              sum = sum * old + l4[i] * f;
+              x[0] = x[0] * old + a4[i].x * f; x[1] = x[1] * old + a4[i].y * f;
+              x[2] = x[2] * old + a4[i].z * f; x[3] = x[3] * old + a4[i].w * f;
+              x[4] = x[4] * old + b4[i].x * f; x[5] = x[5] * old + b4[i].y * f;
+              x[6] = x[6] * old + b4[i].z * f; x[7] = x[7] * old + b4[i].w * f;
+            }
           }
           store(row, d0, x, top, sum);
         }
@@ -461,18 +524,20 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
   if (!ok && lane == 0) atomicOr(p.err, kErrWaitContext);
 }
 
-template <int kDim>
+template <int kDim, int kNt>
 int rows_grid() {
   static PerDevice<int> cache;
   int dev = -1, n = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return -1;
   const bool got = cache.get(dev, [](int* v) {
-    if (cudaFuncSetAttribute(attention_rows_kernel<kDim>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             RowsCfg<kDim>::kSmem) != cudaSuccess)
+    using Cfg = RowsCfg<kDim, kNt>;
+    if (cudaFuncSetAttribute(attention_rows_kernel<kDim, kNt>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             Cfg::kSmem) != cudaSuccess)
       return false;
-    int per_sm = 0, sms = device_sms();
-    if (sms <= 0 || cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attention_rows_kernel<kDim>, kRowsThreads,
-                                                                  RowsCfg<kDim>::kSmem) != cudaSuccess || per_sm < 1)
+    int per_sm = 0;
+    const int sms = device_sms();
+    if (sms <= 0 || cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, attention_rows_kernel<kDim, kNt>,
+                                                                  Cfg::kThreads, Cfg::kSmem) != cudaSuccess || per_sm < 1)
       return false;
     *v = per_sm * sms;
     return true;
@@ -480,25 +545,39 @@ int rows_grid() {
   return got ? n : -1;
 }
 
-// Workspace: the fault latch, the tickets, the split items, the parts.  Sized for both
-// kernels, so that one workspace serves every batch of a shape.
+// Workspace: the fault latch, the tickets, the split items, the parts.  Sized
+// for all kernels, so that one workspace serves every batch of a shape.
 struct AttnWs {
-  int rows_grid, tiles_grid;
+  int grid8, grid16, tiles_grid;  // resident CTAs of the rows kernels and of the tiles kernel
   size_t tickets, splits, part, total;
 };
-bool attn_ws(int dim, AttnWs* w) {
-  w->rows_grid = dim == 128 ? rows_grid<128>() : rows_grid<64>();
-  w->tiles_grid = tiles_grid(dim);
-  if (w->rows_grid < 1 || w->tiles_grid < 1) return false;
-  const size_t rows_floats = dim == 128 ? RowsCfg<128>::kPartFloats : RowsCfg<64>::kPartFloats;
-  const size_t a = static_cast<size_t>(w->rows_grid) * rows_floats, b = w->tiles_grid * tiles_part_floats(dim);
-  const int grid = w->rows_grid > w->tiles_grid ? w->rows_grid : w->tiles_grid;
-  w->tickets = kWsAlign;
+template <int kDim>
+bool attn_ws(AttnWs* w) {
+  w->grid8 = rows_grid<kDim, 1>();
+  w->grid16 = rows_grid<kDim, 2>();
+  w->tiles_grid = tiles_grid(kDim);
+  if (w->grid8 < 1 || w->grid16 < 1 || w->tiles_grid < 1) return false;
   auto up = [](size_t n) { return (n + kWsAlign - 1) / kWsAlign * kWsAlign; };
-  w->splits = w->tickets + up(static_cast<size_t>(grid) * 4);
-  w->part = w->splits + up(static_cast<size_t>(grid) * tiles_split_bytes());
-  w->total = w->part + 2 * sizeof(float) * (a > b ? a : b);
+  auto most = [](size_t a, size_t b) { return a > b ? a : b; };
+  const size_t grid = most(w->grid8, most(w->grid16, w->tiles_grid));
+  const size_t floats = most(w->grid8 * size_t(RowsCfg<kDim, 1>::kPartFloats),
+                             most(w->grid16 * size_t(RowsCfg<kDim, 2>::kPartFloats), w->tiles_grid * tiles_part_floats(kDim)));
+  w->tickets = kWsAlign;
+  w->splits = w->tickets + up(grid * 4);
+  w->part = w->splits + up(grid * tiles_split_bytes());
+  w->total = w->part + 2 * sizeof(float) * floats;
   return true;
+}
+bool attn_ws(int dim, AttnWs* w) { return dim == 128 ? attn_ws<128>(w) : attn_ws<64>(w); }
+
+template <int kDim>
+cudaError_t launch_rows(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& p, bool eight, const AttnWs& ws,
+                        cudaStream_t stream) {
+  if (eight)
+    attention_rows_kernel<kDim, 1><<<ws.grid8, RowsCfg<kDim, 1>::kThreads, RowsCfg<kDim, 1>::kSmem, stream>>>(tmK, tmV, p);
+  else
+    attention_rows_kernel<kDim, 2><<<ws.grid16, RowsCfg<kDim, 2>::kThreads, RowsCfg<kDim, 2>::kSmem, stream>>>(tmK, tmV, p);
+  return cudaGetLastError();
 }
 
 bool shape_ok(int64_t rows, int64_t q_heads, int64_t kv_heads, int dim) {
@@ -584,20 +663,18 @@ dg_status dg_context_attention(const dg_context* ctx, const dg_context_cache* ca
     return DG_ERR_CUDA;
   }
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  // One row tile of the rows kernel is 16 rows; the tiles kernel works on 256
-  // whether they are there or not.
+  // Rows a kv head has in one request at most: the rows kernel takes 8 or 16
+  // at a time, the tiles kernel 256 whether they are there or not.
   const int64_t most = static_cast<int64_t>(max_new > 0 && max_new < ctx->rows ? max_new : ctx->rows) * p.group;
-  if (most > kRowsM) {
+  cudaError_t e;
+  if (most > 16) {
     p.min_tiles = 1;
-    return cuda_ok(launch_attention_tiles(dim, tmK, tmV, p, ws.tiles_grid, cs), "context attention launch") ? DG_OK
-                                                                                                       : DG_ERR_CUDA;
+    e = launch_attention_tiles(dim, tmK, tmV, p, ws.tiles_grid, cs);
+  } else {
+    p.min_tiles = 8;
+    e = dim == 128 ? launch_rows<128>(tmK, tmV, p, most <= 8, ws, cs) : launch_rows<64>(tmK, tmV, p, most <= 8, ws, cs);
   }
-  p.min_tiles = kRowsWarps;
-  if (dim == 128)
-    attention_rows_kernel<128><<<ws.rows_grid, kRowsThreads, RowsCfg<128>::kSmem, cs>>>(tmK, tmV, p);
-  else
-    attention_rows_kernel<64><<<ws.rows_grid, kRowsThreads, RowsCfg<64>::kSmem, cs>>>(tmK, tmV, p);
-  return cuda_ok(cudaGetLastError(), "context attention launch") ? DG_OK : DG_ERR_CUDA;
+  return cuda_ok(e, "context attention launch") ? DG_OK : DG_ERR_CUDA;
 }
 
 }  // extern "C"

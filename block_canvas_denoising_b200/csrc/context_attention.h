@@ -68,10 +68,12 @@ DG_DEV int key_hi(const Request& q, int i) { return q.causal ? q.len - q.nq + i 
 // (one empty tile when none does, so that its zeros get written).  Items in
 // order, each with its key tiles in order, form one line of tiles; every CTA
 // takes an equal piece of that line (per = max(min_tiles, ceil(total /
-// grid)) tiles), whatever requests it spans: ragged batches and single long
+// grid)) units), whatever requests it spans: ragged batches and single long
 // contexts are split evenly by the same rule, and the rule follows the
-// lengths alone.
-template <int kM, int kKeys>
+// lengths alone.  An item is kCost units longer than its tiles, for what it
+// costs beside them (queries, result): they lie ahead of its first tile, and
+// nobody works on them.
+template <int kM, int kKeys, int kCost>
 struct Split {
   static DG_DEV int row_tiles(const AttnParams& p, const Request& q) {
     return static_cast<int>((static_cast<int64_t>(q.nq) * p.group + kM - 1) / kM);
@@ -110,14 +112,15 @@ struct Split {
       } else {
         n = -1;
       }
-      before[r + 1] = n < 0 ? n : n * p.kv_heads;
+      before[r + 1] = n < 0 ? n : (n + static_cast<int64_t>(mts) * kCost) * p.kv_heads;
     }
     if (threadIdx.x == 0) before[0] = 0;
     __syncthreads();
     for (int r = threadIdx.x >> 5; r < p.B; r += blockDim.x >> 5) {
       if (before[r + 1] >= 0) continue;  // the same for the whole warp
       const Request q = request_of(p, r);
-      const int64_t n = warp_tiles(p, q, row_tiles(p, q));
+      const int mts = row_tiles(p, q);
+      const int64_t n = warp_tiles(p, q, mts) + static_cast<int64_t>(mts) * kCost;
       if ((threadIdx.x & 31) == 0) before[r + 1] = n * p.kv_heads;
     }
     __syncthreads();
@@ -141,10 +144,10 @@ struct Split {
 
   int r, mt, h;          // the item
   Request q;
-  int64_t begin;         // its first tile on the line
+  int64_t begin;         // its first tile on the line (behind its cost)
   int tiles, first;      // its key tiles: first, first + 1, ...
-  // The item that holds tile `pos` of the line.  All lanes of a warp, with
-  // the same arguments.
+  // The item that holds unit `pos` of the line.  All lanes of a warp, with the
+  // same arguments.
   DG_DEV void find(const AttnParams& p, const int64_t* before, int64_t pos) {
     int lo = 0, hi = p.B - 1;
     while (lo < hi) {
@@ -159,17 +162,17 @@ struct Split {
     begin = before[r];
     if (!q.causal && p.window == 0) {  // every row tile sees the same keys
       tiles = item_tiles(p, q, 0, &first);
-      const int64_t n = (pos - begin) / tiles;
+      const int64_t n = (pos - begin) / (tiles + kCost);
       mt = static_cast<int>(n / p.kv_heads);
       h = static_cast<int>(n % p.kv_heads);
-      begin += n * tiles;
+      begin += n * (tiles + kCost) + kCost;
       return;
     }
     const int lane = static_cast<int>(threadIdx.x & 31);
     const int mts = row_tiles(p, q);
     for (int m0 = 0;; m0 += 32) {  // 32 row tiles at a time
       int f = 0;
-      const int n = m0 + lane < mts ? item_tiles(p, q, m0 + lane, &f) : 0;
+      const int n = m0 + lane < mts ? item_tiles(p, q, m0 + lane, &f) + kCost : 0;
       int64_t upto = static_cast<int64_t>(n) * p.kv_heads;
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -182,12 +185,13 @@ struct Split {
         continue;
       }
       const int at = behind == 0 ? 31 : __ffs(behind) - 1;
-      tiles = __shfl_sync(0xffffffffu, n, at);
+      const int units = __shfl_sync(0xffffffffu, n, at);
       first = __shfl_sync(0xffffffffu, f, at);
-      begin += __shfl_sync(0xffffffffu, upto, at) - static_cast<int64_t>(tiles) * p.kv_heads;
+      begin += __shfl_sync(0xffffffffu, upto, at) - static_cast<int64_t>(units) * p.kv_heads;
       mt = m0 + at;
-      h = static_cast<int>((pos - begin) / tiles);
-      begin += static_cast<int64_t>(h) * tiles;
+      h = static_cast<int>((pos - begin) / units);
+      begin += static_cast<int64_t>(h) * units + kCost;
+      tiles = units - kCost;
       return;
     }
   }

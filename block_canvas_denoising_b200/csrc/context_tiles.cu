@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kTilesThreads, 1)
 attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const __grid_constant__ AttnParams p) {
   using Cfg = TilesCfg<kDim>;
-  using S = Split<kTilesM, kTilesN>;
+  using S = Split<kTilesM, kTilesN, 6>;  // queries and result of an item take as long as some 6 tiles
   extern __shared__ uint8_t smem_raw[];
   __shared__ TilesShared sh;
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -493,10 +493,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       Piece w;
+      S it;
+      if (pos < end) {
+        it.find(p, sh.before, pos);
+        pos = max(pos, it.begin);
+      }
       w.last = pos >= end;
       if (!w.last) {
-        S it;
-        it.find(p, sh.before, pos);
         const int64_t item_end = it.begin + it.tiles;
         w.r = it.r;
         w.row0 = it.q.row0;
