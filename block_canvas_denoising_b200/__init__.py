@@ -591,30 +591,27 @@ def _need(ok: bool, what: str) -> None:
         raise DGError(1, what)
 
 
-def _on(device, stream):
-    """The stream handle to launch on for tensors of ``device``."""
+def _call(device, fn, where, stream, *args):
+    """Call a library function on ``stream`` (None: the current one) with the
+    tensors' device current."""
     import torch
     if stream is None:
-        return torch.cuda.current_stream(device).cuda_stream
-    _need(stream.device == device, "the stream belongs to another device than the tensors")
-    return stream.cuda_stream
-
-
-def _call(device, fn, where, *args):
-    """Call a library function with the tensors' device current."""
-    import torch
-    if torch.cuda.current_device() == device.index:
-        code = fn(*args)
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    else:
+        _need(stream.device == device, "the stream belongs to another device than the tensors")
+        handle = stream.cuda_stream
+    if torch._C._cuda_getDevice() == device.index:
+        code = fn(*args, handle)
     else:
         with torch.cuda.device(device):
-            code = fn(*args)
+            code = fn(*args, handle)
     if code != 0:
         _check(code, where)
 
 
 def _heads(t, rows, heads, dim, device, name) -> _Heads:
     import torch
-    if t.dtype != torch.bfloat16 or t.dim() != 3 or t.device != device:
+    if t.dtype is not torch.bfloat16 or t.dim() != 3 or t.device != device:
         raise DGError(1, f"{name} must be a bfloat16 tensor [rows, heads, dim] on {device}")
     n, h, d = t.shape
     rs, hs, ds = t.stride()
@@ -625,9 +622,10 @@ def _heads(t, rows, heads, dim, device, name) -> _Heads:
         hs = dim
     if n == 1:
         rs = max(rs if rs % 8 == 0 else 0, dim)
-    if ds != 1 or rs < dim or (h > 1 and hs < dim) or rs % 8 or hs % 8 or t.data_ptr() % 16:
+    ptr = t.data_ptr()
+    if ds != 1 or rs < dim or (h > 1 and hs < dim) or rs % 8 or hs % 8 or ptr % 16:
         raise DGError(1, f"{name} needs contiguous heads, strides of multiples of 8 elements and 16-byte alignment")
-    return _Heads(t.data_ptr(), rs, hs)
+    return _Heads(ptr, rs, hs)
 
 
 class ContextPlan:
@@ -674,8 +672,8 @@ def context_plan(plan: ContextPlan, add, release=None, commit: bool = False, str
     _need(release is None or (release.dtype in (torch.uint8, torch.bool) and release.shape == (plan.B,) and
                               release.is_contiguous() and release.device == plan.device),
           "release must be a contiguous uint8 tensor [B] on the plan's device")
-    _call(plan.device, lib().dg_context_plan, "dg_context_plan", plan._ref, add.data_ptr(),
-          None if release is None else release.data_ptr(), 1 if commit else 0, _on(plan.device, stream))
+    _call(plan.device, lib().dg_context_plan, "dg_context_plan", stream, plan._ref, add.data_ptr(),
+          None if release is None else release.data_ptr(), 1 if commit else 0)
 
 
 def context_status(plan: ContextPlan, stream=None) -> int:
@@ -683,7 +681,7 @@ def context_status(plan: ContextPlan, stream=None) -> int:
     was refused) or 9 (an append met a value that is not finite; cleared)."""
     import torch
     with torch.cuda.device(plan.device):
-        return int(lib().dg_context_status(plan._ref, _on(plan.device, stream)))
+        return int(lib().dg_context_status(plan._ref, _stream(stream)))
 
 
 class RopeFrequencies:
@@ -720,8 +718,8 @@ def rope(x, positions, frequencies: RopeFrequencies, out=None, stream=None):
     if rows == 0:
         return out
     a, b = _heads(x, rows, heads, dim, x.device, "x"), _heads(out, rows, heads, dim, x.device, "out")
-    _call(x.device, lib().dg_rope, "dg_rope", ctypes.byref(a), ctypes.byref(b), rows, heads, dim,
-          positions.data_ptr(), frequencies._ref, _on(x.device, stream))
+    _call(x.device, lib().dg_rope, "dg_rope", stream, ctypes.byref(a), ctypes.byref(b), rows, heads, dim,
+          positions.data_ptr(), frequencies._ref)
     return out
 
 
@@ -754,8 +752,8 @@ def context_append(plan: ContextPlan, cache: ContextCache, k, v, rope: RopeFrequ
           "the cache and the frequencies must be on the plan's device")
     a = _heads(k, plan.rows, cache.heads, cache.dim, dev, "k")
     b = _heads(v, plan.rows, cache.heads, cache.dim, dev, "v")
-    _call(dev, lib().dg_context_append, "dg_context_append", plan._ref, cache._ref, ctypes.byref(a), ctypes.byref(b),
-          None if rope is None else rope._ref, _on(dev, stream))
+    _call(dev, lib().dg_context_append, "dg_context_append", stream, plan._ref, cache._ref, ctypes.byref(a),
+          ctypes.byref(b), None if rope is None else rope._ref)
 
 
 def context_workspace_size(rows: int, q_heads: int, kv_heads: int, dim: int) -> int:
@@ -800,9 +798,9 @@ def context_attention(plan: ContextPlan, cache: ContextCache, q, out, ws: Contex
                           lse.shape[1] == heads and lse.is_contiguous() and lse.device == dev),
           "lse must be a contiguous float32 tensor [rows, heads] on the plan's device")
     _need(scale is None or scale > 0, "scale must be positive")
-    _call(dev, lib().dg_context_attention, "dg_context_attention", plan._ref, cache._ref, ctypes.byref(a),
+    _call(dev, lib().dg_context_attention, "dg_context_attention", stream, plan._ref, cache._ref, ctypes.byref(a),
           ctypes.byref(b), heads, 0.0 if scale is None else scale, None if causal is None else causal.data_ptr(),
-          window, max_new, None if lse is None else lse.data_ptr(), ws.buf.data_ptr(), ws.nbytes, _on(dev, stream))
+          window, max_new, None if lse is None else lse.data_ptr(), ws.buf.data_ptr(), ws.nbytes)
 
 
 def debug_gumbel(words, stream=None):

@@ -92,6 +92,8 @@ context_plan_kernel(const dg_context c, const int32_t* __restrict__ add, const u
   const int64_t room = static_cast<int64_t>(c.max_pages) * DG_PAGE;
   if (tid == 0) s_bad = 0;
   __syncthreads();
+  wait_for_previous_kernel();
+  allow_next_kernel();
 
   const int64_t free0 = *(commit ? c.free_next : c.free_count);
   int64_t held = 0, a = 0, gone = 0, need = 0, touched = 0;
@@ -148,28 +150,36 @@ context_plan_kernel(const dg_context c, const int32_t* __restrict__ add, const u
     return j < first ? c.table[static_cast<size_t>(r) * c.max_pages + j]
                      : c.free_list[free1 - 1 - s_need0[r] - (j - first)];
   };
-  for (int i = gtid; i < c.rows; i += gsize) {
-    int pos = -1;
-    int64_t slot = -1;
-    if (i < total) {
-      const int r = owner_of(s_start, B, i);
-      pos = s_held[r] + i - s_start[r];
-      slot = static_cast<int64_t>(page_of(r, pos / DG_PAGE)) * DG_PAGE + pos % DG_PAGE;
-    }
-    c.positions[i] = pos;
-    c.slots[i] = slot;
-  }
+  // Rows by their runs: a lane finds one run's request and page (a search and
+  // a read, 32 of them at once), and the warp then writes the rows of each.
   const int runs = DG_CONTEXT_RUNS(c.rows, B), used = s_run0[B];
-  for (int u = gtid; u < runs; u += gsize) {
+  for (int u0 = warp; u0 < runs; u0 += 32 * warps) {
+    const int u = u0 + lane * warps;
     int4 run = make_int4(-1, 0, 0, 0);
+    int pos = 0;
     if (u < used) {
       const int r = owner_of(s_run0, B, u);
       const int h = s_held[r], end = h + s_start[r + 1] - s_start[r];
       const int j = h / DG_PAGE + u - s_run0[r];
       const int lo = max(j * DG_PAGE, h), hi = min((j + 1) * DG_PAGE, end);
       run = make_int4(page_of(r, j), s_start[r] + lo - h, lo - j * DG_PAGE, hi - lo);
+      pos = lo;
     }
-    reinterpret_cast<int4*>(c.runs)[u] = run;
+    if (u < runs) reinterpret_cast<int4*>(c.runs)[u] = run;
+    const int n = min(32, (used - u0 + warps - 1) / warps);  // runs the warp has in hand
+    for (int k = 0; k < n; ++k) {
+      const int page = __shfl_sync(0xffffffffu, run.x, k), row = __shfl_sync(0xffffffffu, run.y, k);
+      const int off = __shfl_sync(0xffffffffu, run.z, k), count = __shfl_sync(0xffffffffu, run.w, k);
+      const int first = __shfl_sync(0xffffffffu, pos, k);
+      for (int i = lane; i < count; i += 32) {
+        c.positions[row + i] = first + i;
+        c.slots[row + i] = static_cast<int64_t>(page) * DG_PAGE + off + i;
+      }
+    }
+  }
+  for (int i = total + gtid; i < c.rows; i += gsize) {
+    c.positions[i] = -1;
+    c.slots[i] = -1;
   }
   for (int r = warp; r < B; r += warps) {
     const int first = (s_held[r] + DG_PAGE - 1) / DG_PAGE;
@@ -195,17 +205,38 @@ context_plan_kernel(const dg_context c, const int32_t* __restrict__ add, const u
 // ---------------------------------------------------------------------------
 // rotary positions
 // ---------------------------------------------------------------------------
-// cos and sin of position * freq, times the magnitude.  The product and its
-// reduction to a fraction of a turn are in float64 (a float32 product is off
-// by more than a hundredth of a radian at positions in the hundred
-// thousands); the fraction, at most half a turn, is then exact enough in
-// float32 for sincospif.
-DG_DEV float2 turn_of(int position, double freq, float magnitude) {
-  double t = static_cast<double>(position) * freq * 0.15915494309189533577;  // 1 / (2 pi)
-  t -= rint(t);
-  float s, c;
-  sincospif(2.0f * static_cast<float>(t), &s, &c);
-  return make_float2(c * magnitude, s * magnitude);
+// A frequency as a fraction of a turn per position, in units of 2^-64: then
+// position * turn, mod 2^64, is the exact place within a turn of a frequency
+// that is off by at most 2^-64 + 2^-53 of itself (a float32 product is off by
+// more than a hundredth of a radian at positions in the hundred thousands).
+DG_DEV uint64_t turn_fraction(double freq) {
+  double f = freq * 0.15915494309189533577;  // 1 / (2 pi)
+  f -= floor(f);
+  const uint32_t hi = static_cast<uint32_t>(f * 4294967296.0);  // f < 1
+  const uint32_t lo = static_cast<uint32_t>((f * 4294967296.0 - hi) * 4294967296.0);
+  return static_cast<uint64_t>(hi) << 32 | lo;
+}
+// (cos, sin) of a place within a turn, times the magnitude.  The nearest
+// quarter turn goes off by integer arithmetic, and the rest, at most pi / 4,
+// through the Taylor polynomials of degree 9 and 8, whose remainders there are
+// (pi/4)^11 / 11! = 2e-9 and (pi/4)^10 / 10! = 3e-8, half a float32 step of 1.
+DG_DEV float2 turn_of(uint64_t place, float magnitude) {
+  const uint32_t p = static_cast<uint32_t>(place >> 32);
+  const uint32_t quarter = (p + 0x20000000u) >> 30;
+  const float x = static_cast<float>(static_cast<int32_t>(p - (quarter << 30))) * 1.4629180792671596e-9f;  // 2 pi / 2^32
+  const float z = x * x;
+  float s = fmaf(z, 2.7557319223985893e-6f, -1.9841269841269841e-4f);
+  s = fmaf(z, s, 8.3333333333333333e-3f);
+  s = fmaf(z, s, -0.16666666666666667f);
+  s = fmaf(z * x, s, x);
+  float c = fmaf(z, 2.4801587301587302e-5f, -1.3888888888888889e-3f);
+  c = fmaf(z, c, 4.1666666666666667e-2f);
+  c = fmaf(z, c, -0.5f);
+  c = fmaf(z, c, 1.0f);
+  const float co = (quarter & 1) ? s : c, si = (quarter & 1) ? c : s;
+  // quarters: (c, s), (-s, c), (-c, -s), (s, -c)
+  return make_float2((quarter == 1 || quarter == 2) ? -co * magnitude : co * magnitude,
+                     (quarter == 2 || quarter == 3) ? -si * magnitude : si * magnitude);
 }
 
 DG_DEV void unpack8(const uint4& w, float (&x)[8]) {
@@ -257,69 +288,125 @@ DG_DEV void rotate_unit(float (&a)[8], float (&b)[8], const float2 (&t)[8], bool
   }
 }
 
+// Where the turn of frequency j = 8 u + 2 k + w lies in a token's row of turns,
+// `units` units long: pair k of all units side by side, so that neighbouring
+// threads (units) read neighbouring 16 bytes.
+DG_DEV int turn_place(int j, int units) { return (((j >> 1) & 3) * units + (j >> 3)) * 2 + (j & 1); }
+// The eight turns of unit u.
+DG_DEV void read_turns(const float2* row, int u, int units, float2 (&t)[8]) {
+#pragma unroll
+  for (int k = 0; k < 4; ++k)
+    *reinterpret_cast<float4*>(&t[2 * k]) = *reinterpret_cast<const float4*>(&row[(k * units + u) * 2]);
+}
+
 constexpr int kRopeThreads = 256;
 
 // kTokens token rows per CTA.  The turns of a token serve all of its heads:
 // they are formed once, by one thread per (token, frequency), and kept in
-// shared memory; the heads then stream through, 32 bytes a thread.
-template <int kTokens>
+// shared memory; the heads then stream through, 32 bytes a thread, a thread
+// staying on its unit and walking the (token, head) pairs by a fixed stride
+// (256 threads / units = step_tokens * heads + step_heads), without a division (with one per item the integer pipe was the bound: 14.6 us for
+// 8191 rows x 16 heads).
+template <int kDim, int kTokens>
 __global__ void __launch_bounds__(kRopeThreads)
-rope_kernel(const uint8_t* x, uint8_t* out, int64_t xr, int64_t xh, int64_t outr, int64_t outh, int rows,
-            int heads, int dim, const int32_t* __restrict__ positions, const double* __restrict__ freq, int rot,
-            int interleaved, float magnitude) {
-  __shared__ float2 turns[kTokens][64];
+rope_kernel(const uint8_t* x, uint8_t* out, int64_t xr, int64_t xh, int64_t outr, int64_t outh, int rows, int heads,
+            int step_tokens, int step_heads, const int32_t* __restrict__ positions, const double* __restrict__ freq,
+            int rot, int interleaved, float magnitude) {
+  constexpr int kUnits = kDim / 16;                 // units per head
+  __shared__ __align__(16) float2 turns[kTokens][kDim / 2];
   __shared__ int s_pos[kTokens];
   const int row0 = blockIdx.x * kTokens;
-  const int half = rot / 2;
-  for (int i = threadIdx.x; i < kTokens * half; i += kRopeThreads) {
-    const int t = i / half, j = i - t * half;
-    if (row0 + t < rows) turns[t][j] = turn_of(positions[row0 + t], freq[j], magnitude);
+  const int half = rot / 2, rot16 = rot / 16;
+  const int u = threadIdx.x % kUnits;
+  int ca, cb;
+  unit_chunks(u, rot16, interleaved, ca, cb);
+  const bool turned = u < rot16, idle = x == out && !turned;
+  const int tokens = min(kTokens, rows - row0);
+  x += 2 * row0 * xr;
+  out += 2 * row0 * outr;
+  // this thread's first pair
+  int token = 0, head = threadIdx.x / kUnits;
+  while (head >= heads) {
+    head -= heads;
+    ++token;
   }
-  if (threadIdx.x < kTokens) s_pos[threadIdx.x] = row0 + threadIdx.x < rows ? positions[row0 + threadIdx.x] : -1;
-  __syncthreads();
-  const int units = dim / 16, rot16 = rot / 16;
-  const int per_token = heads * units;
-  const bool in_place = x == out;
-  for (int i = threadIdx.x; i < kTokens * per_token; i += kRopeThreads) {
-    const int t = i / per_token, rest = i - t * per_token;
-    const int h = rest / units, u = rest - h * units;
-    if (s_pos[t] < 0 || (in_place && u >= rot16)) continue;
-    int ca, cb;
-    unit_chunks(u, rot16, interleaved, ca, cb);
-    const uint8_t* src = x + 2 * ((row0 + t) * xr + h * xh);
-    uint8_t* dst = out + 2 * ((row0 + t) * outr + h * outh);
-    uint4 wa = *reinterpret_cast<const uint4*>(src + 16 * ca), wb = *reinterpret_cast<const uint4*>(src + 16 * cb);
-    if (u < rot16) {
-      float a[8], b[8];
-      unpack8(wa, a);
-      unpack8(wb, b);
-      float2 tr[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) tr[j] = turns[t][8 * u + j];
-      rotate_unit(a, b, tr, interleaved);
-      wa = pack8(a);
-      wb = pack8(b);
+  auto next = [&](int& t, int& h) {
+    t += step_tokens;
+    h += step_heads;
+    if (h >= heads) {
+      h -= heads;
+      ++t;
     }
-    *reinterpret_cast<uint4*>(dst + 16 * ca) = wa;
-    *reinterpret_cast<uint4*>(dst + 16 * cb) = wb;
+  };
+  auto load = [&](int t, int h, uint4& a, uint4& b) {
+    const uint8_t* src = x + 2 * (t * xr + h * xh);
+    a = *reinterpret_cast<const uint4*>(src + 16 * ca);
+    b = *reinterpret_cast<const uint4*>(src + 16 * cb);
+  };
+  wait_for_previous_kernel();
+  allow_next_kernel();
+  // the first two are on their way while the turns are formed
+  uint4 wa[2], wb[2];
+  {
+    int t = token, h = head;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      if (t < tokens && !idle) load(t, h, wa[k], wb[k]);
+      next(t, h);
+    }
+  }
+  for (int i = threadIdx.x; i < tokens * half; i += kRopeThreads) {
+    const int t = i / half, j = i - t * half;
+    turns[t][turn_place(j, rot16)] =
+        turn_of(static_cast<uint32_t>(positions[row0 + t]) * turn_fraction(freq[j]), magnitude);
+  }
+  if (threadIdx.x < kTokens) s_pos[threadIdx.x] = threadIdx.x < tokens ? positions[row0 + threadIdx.x] : -1;
+  __syncthreads();
+  if (idle) return;
+  for (int k = 0; token < tokens; k ^= 1) {
+    uint4 va = k ? wa[1] : wa[0], vb = k ? wb[1] : wb[0];
+    {  // the one after the next
+      int t = token, h = head;
+      next(t, h);
+      next(t, h);
+      if (t < tokens) {
+        if (k)
+          load(t, h, wa[1], wb[1]);
+        else
+          load(t, h, wa[0], wb[0]);
+      }
+    }
+    if (s_pos[token] >= 0) {
+      if (turned) {
+        float a[8], b[8];
+        unpack8(va, a);
+        unpack8(vb, b);
+        float2 tr[8];
+        read_turns(turns[token], u, rot16, tr);
+        rotate_unit(a, b, tr, interleaved);
+        va = pack8(a);
+        vb = pack8(b);
+      }
+      uint8_t* dst = out + 2 * (token * outr + head * outh);
+      *reinterpret_cast<uint4*>(dst + 16 * ca) = va;
+      *reinterpret_cast<uint4*>(dst + 16 * cb) = vb;
+    }
+    next(token, head);
   }
 }
 
 // ---------------------------------------------------------------------------
 // append
 // ---------------------------------------------------------------------------
-constexpr int kAppendThreads = 256;
-
-// The least power of two s with top <= 448 s, at least 2^-100; 1 for 0.
-// 448 = 0.875 * 2^9, so with top = f 2^e (f in [0.5, 1)) s is 2^(e - 9) for
-// f <= 0.875 and 2^(e - 8) above.
-DG_DEV float scale_of(float top) {
-  if (top == 0.f) return 1.f;
-  int e;
-  const float f = frexpf(top, &e);
-  e = max(e - 9 + (f > 0.875f ? 1 : 0), -100);
-  return ldexpf(1.f, e);
+// The exponent of the least power of two s with top <= 448 s, at least -100;
+// 0 for top = 0.  448 = 1.75 * 2^8, so with top = 1.m 2^E it is E - 8, and one
+// more where 1.m is above 1.75 (a top that is subnormal ends at -100 anyway).
+DG_DEV int scale_exponent(float top) {
+  if (top == 0.f) return 0;
+  const uint32_t b = __float_as_uint(top);
+  return max(static_cast<int>(b >> 23) - 135 + ((b & 0x7FFFFFu) > 0x600000u ? 1 : 0), -100);
 }
+DG_DEV float power_of_two(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }  // -126 <= e <= 127
 // Two floats to E4M3, to nearest even, saturating; NaN stays NaN.
 DG_DEV uint32_t e4m3_pair(float lo, float hi) {
   return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
@@ -329,95 +416,158 @@ DG_DEV uint2 e4m3_chunk(const float (&x)[8], float inv) {
                     e4m3_pair(x[4] * inv, x[5] * inv) | e4m3_pair(x[6] * inv, x[7] * inv) << 16);
 }
 
-// One CTA per (run, kv head, k or v): it owns the page's scale and all of
-// its codes, so no two CTAs meet.  The run's values stay in registers
-// between the two things that need them, the largest magnitude and the
-// codes: 64 rows x 128 elements are 32 floats a thread.
+// One CTA per (run, `per` kv heads, k or v): it owns those pages' scales and
+// all of their codes, so no two CTAs meet.  A thread has kMine units of 16
+// elements (a run of 64 rows fills the block); they stay in registers between
+// the two things that need them, the largest magnitude and the codes, and the
+// next head's are on their way meanwhile.  The turns of the run's tokens serve
+// all of its heads.  Many rows: as many heads a CTA as give one wave over the
+// device; few: one, for the latency, each thread forming its own turns.
+constexpr int kMine = 2;
 template <int kDim>
-__global__ void __launch_bounds__(kAppendThreads)
+constexpr int kAppendThreads = DG_PAGE * kDim / 16 / kMine;
+
+template <int kDim, bool kShare>
+__global__ void __launch_bounds__(kAppendThreads<kDim>)
 context_append_kernel(const dg_context c, const dg_context_cache cache, const dg_heads kin, const dg_heads vin,
-                      const dg_rope_args rope, int has_rope) {
-  constexpr int kUnits = kDim / 16;                                  // units per row
-  constexpr int kMine = DG_PAGE * kUnits / kAppendThreads;           // units per thread
-  __shared__ float s_top[kAppendThreads / 32];
+                      const dg_rope_args rope, int has_rope, int per) {
+  constexpr int kUnits = kDim / 16;  // units per row
+  constexpr int kThreads = kAppendThreads<kDim>, kWarps = kThreads / 32;
+  constexpr int kRows = kThreads / kUnits;        // rows between a thread's units
+  constexpr int kPairs = kShare ? kDim / 2 : 1;   // turns kept per token
+  __shared__ float s_top[3][kWarps];
+  __shared__ __align__(16) float2 s_turn[kShare ? DG_PAGE : 1][kPairs];
+  wait_for_previous_kernel();
+  allow_next_kernel();
   const int4 run = reinterpret_cast<const int4*>(c.runs)[blockIdx.x];
   const int page = run.x, row0 = run.y, off = run.z, n = run.w;
   if (page < 0 || page >= cache.pages || n <= 0 || off < 0 || off + n > DG_PAGE || row0 < 0 || row0 + n > c.rows) return;
-  const int head = blockIdx.y;
+  const int head0 = blockIdx.y * per, heads = min(per, cache.heads - head0);
   const bool is_k = blockIdx.z == 0;
   const dg_heads& in = is_k ? kin : vin;
-  float* scale_at = (is_k ? cache.k_scale : cache.v_scale) + static_cast<size_t>(page) * cache.heads + head;
-  uint8_t* codes = (is_k ? cache.k : cache.v) + (static_cast<size_t>(page) * cache.heads + head) * DG_PAGE * kDim;
   const int rot16 = (is_k && has_rope) ? rope.rot / 16 : 0;
   const bool il = rope.interleaved != 0;
+  const int row = threadIdx.x / kUnits, u = threadIdx.x % kUnits;  // of the thread's first unit
+  const bool turned = u < rot16;
+  int ca, cb;
+  unit_chunks(u, rot16, il, ca, cb);
+  const size_t at0 = static_cast<size_t>(page) * cache.heads + head0;
+  float* scale = (is_k ? cache.k_scale : cache.v_scale) + at0;
+  uint8_t* codes = (is_k ? cache.k : cache.v) + at0 * DG_PAGE * kDim;
+  const uint8_t* src = static_cast<const uint8_t*>(in.data) + 2 * ((row0 + row) * in.row_stride + head0 * in.head_stride);
+  const int64_t row_step = 2 * kRows * in.row_stride, head_step = 2 * in.head_stride;
 
-  float a[kMine][8], b[kMine][8];
-  float top = 0.f;
-  bool odd = false;
+  uint4 wa[kMine] = {}, wb[kMine] = {};
+  auto load = [&](const uint8_t* from) {
 #pragma unroll
-  for (int m = 0; m < kMine; ++m) {
-    const int i = threadIdx.x + m * kAppendThreads;
-    const int row = i / kUnits, u = i % kUnits;
-    if (row >= n) continue;
-    int ca, cb;
-    unit_chunks(u, rot16, il, ca, cb);
-    const uint8_t* src = static_cast<const uint8_t*>(in.data) + 2 * ((row0 + row) * in.row_stride + head * in.head_stride);
-    unpack8(*reinterpret_cast<const uint4*>(src + 16 * ca), a[m]);
-    unpack8(*reinterpret_cast<const uint4*>(src + 16 * cb), b[m]);
-    if (u < rot16) {
-      const int pos = c.positions[row0 + row];
-      float2 tr[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) tr[j] = turn_of(pos, rope.freq[8 * u + j], rope.magnitude);
-      rotate_unit(a[m], b[m], tr, il);
+    for (int m = 0; m < kMine; ++m) {
+      if (row + m * kRows >= n) continue;
+      wa[m] = *reinterpret_cast<const uint4*>(from + m * row_step + 16 * ca);
+      wb[m] = *reinterpret_cast<const uint4*>(from + m * row_step + 16 * cb);
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float x = fabsf(a[m][j]), y = fabsf(b[m][j]);
-      if (x <= FLT_MAX) top = fmaxf(top, x); else odd = true;
-      if (y <= FLT_MAX) top = fmaxf(top, y); else odd = true;
-      if (a[m][j] != a[m][j]) a[m][j] = 0.f;
-      if (b[m][j] != b[m][j]) b[m][j] = 0.f;
-    }
+  };
+  load(src);
+  if (kShare && rot16 > 0) {
+    const int half = 8 * rot16, stride = kThreads / half;
+    const int j = threadIdx.x % half;  // this thread's frequency; the block's threads walk the rows
+    const uint64_t turn = turn_fraction(rope.freq[j]);
+    const uint32_t pos = c.positions[row0];  // a run's tokens follow one another
+    for (int r = threadIdx.x / half; r < n && static_cast<int>(threadIdx.x) < stride * half; r += stride)
+      s_turn[r][turn_place(j, rot16)] = turn_of((pos + r) * turn, rope.magnitude);
+    __syncthreads();
   }
+  for (int h = 0; h < heads; ++h, ++scale, codes += DG_PAGE * kDim) {
+    const float old = *scale;
+    float a[kMine][8], b[kMine][8];
 #pragma unroll
-  for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-  if ((threadIdx.x & 31) == 0) s_top[threadIdx.x >> 5] = top;
-  if (__any_sync(0xffffffffu, odd) && (threadIdx.x & 31) == 0) atomicOr(reinterpret_cast<unsigned*>(c.status + 1), 1u);
-  const float old = *scale_at;
-  __syncthreads();
-  top = s_top[0];
+    for (int m = 0; m < kMine; ++m) {
+      unpack8(wa[m], a[m]);
+      unpack8(wb[m], b[m]);
+    }
+    src += head_step;
+    if (h + 1 < heads) load(src);
+    if (turned) {
 #pragma unroll
-  for (int w = 1; w < kAppendThreads / 32; ++w) top = fmaxf(top, s_top[w]);
-  float s = scale_of(top);
-  if (off > 0 && !(s > old)) s = old;
-  if (off > 0 && s > old) {  // kept tokens move to the larger scale
-    const float ratio = old / s;
-    for (int i = threadIdx.x; i < off * kDim / 4; i += kAppendThreads) {
-      const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[i];
-      float f[4];
+      for (int m = 0; m < kMine; ++m) {
+        if (row + m * kRows >= n) continue;
+        float2 tr[8];
+        if (kShare) {
+          read_turns(s_turn[row + m * kRows], u, rot16, tr);
+        } else {
+          const uint32_t pos = c.positions[row0] + row + m * kRows;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __half_raw hr = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(w >> (8 * j)), __NV_E4M3);
-        f[j] = __half2float(*reinterpret_cast<const __half*>(&hr)) * ratio;
+          for (int j = 0; j < 8; ++j) tr[j] = turn_of(pos * turn_fraction(rope.freq[8 * u + j]), rope.magnitude);
+        }
+        rotate_unit(a[m], b[m], tr, il);
       }
-      reinterpret_cast<uint32_t*>(codes)[i] = e4m3_pair(f[0], f[1]) | e4m3_pair(f[2], f[3]) << 16;
     }
-  }
-  const float inv = 1.0f / s;  // exact: s is a power of two
+    float top = 0.f, zero = 0.f, zero2 = 0.f;  // sums of 0 x: NaN if some x is not finite
 #pragma unroll
-  for (int m = 0; m < kMine; ++m) {
-    const int i = threadIdx.x + m * kAppendThreads;
-    const int row = i / kUnits, u = i % kUnits;
-    if (row >= n) continue;
-    int ca, cb;
-    unit_chunks(u, rot16, il, ca, cb);
+    for (int m = 0; m < kMine; ++m) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        top = fmaxf(top, fmaxf(fabsf(a[m][j]), fabsf(b[m][j])));
+        zero = fmaf(a[m][j], 0.f, zero);
+        zero2 = fmaf(b[m][j], 0.f, zero2);
+      }
+    }
+    zero += zero2;
+    // The largest over the block; infinite if anything is not finite.  The
+    // barrier also has every thread past its read of the old scale.
+    auto largest = [&](int buffer) {
+      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));  // not negative: ordered as integers
+      if ((threadIdx.x & 31) == 0) s_top[buffer][threadIdx.x >> 5] = top;
+      __syncthreads();
+      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s_top[buffer][threadIdx.x & (kWarps - 1)])));
+    };
+    if (zero != zero) top = INFINITY;
+    largest(h & 1);
+    if (top > FLT_MAX) {  // seldom: what is not finite does not count, NaN becomes 0
+      top = 0.f;
+#pragma unroll
+      for (int m = 0; m < kMine; ++m) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float x = fabsf(a[m][j]), y = fabsf(b[m][j]);
+          if (x <= FLT_MAX) top = fmaxf(top, x);
+          if (y <= FLT_MAX) top = fmaxf(top, y);
+          if (a[m][j] != a[m][j]) a[m][j] = 0.f;
+          if (b[m][j] != b[m][j]) b[m][j] = 0.f;
+        }
+      }
+      largest(2);
+      if (threadIdx.x == 0) atomicOr(reinterpret_cast<unsigned*>(c.status + 1), 1u);
+      __syncthreads();  // the third buffer may be used again
+    }
+    const int e = scale_exponent(top);
+    float s = power_of_two(e), inv = power_of_two(-e);  // |e| <= 120
+    if (off > 0) {
+      if (!(s > old)) {
+        s = old;
+        inv = 1.0f / old;  // exact: a power of two
+      } else {  // kept tokens move to the larger scale
+        const float ratio = old / s;
+        for (int i = threadIdx.x; i < off * kDim / 4; i += kThreads) {
+          const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[i];
+          float f[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __half_raw hr = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(w >> (8 * j)), __NV_E4M3);
+            f[j] = __half2float(*reinterpret_cast<const __half*>(&hr)) * ratio;
+          }
+          reinterpret_cast<uint32_t*>(codes)[i] = e4m3_pair(f[0], f[1]) | e4m3_pair(f[2], f[3]) << 16;
+        }
+      }
+    }
     uint8_t* dst = codes + (off + row) * kDim;
-    *reinterpret_cast<uint2*>(dst + 8 * ca) = e4m3_chunk(a[m], inv);
-    *reinterpret_cast<uint2*>(dst + 8 * cb) = e4m3_chunk(b[m], inv);
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+      if (row + m * kRows >= n) continue;
+      *reinterpret_cast<uint2*>(dst + m * kRows * kDim + 8 * ca) = e4m3_chunk(a[m], inv);
+      *reinterpret_cast<uint2*>(dst + m * kRows * kDim + 8 * cb) = e4m3_chunk(b[m], inv);
+    }
+    if (threadIdx.x == 0) *scale = s;
   }
-  __syncthreads();  // every thread has read the old scale
-  if (threadIdx.x == 0) *scale_at = s;
 }
 
 bool aligned(const void* p, uintptr_t n) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
@@ -473,8 +623,11 @@ dg_status dg_context_plan(const dg_context* ctx, const int32_t* add, const uint8
   if (st != DG_OK) return st;
   if (!aligned(add, 4)) return DG_ERR_INVALID_ARG;
   if (device_sms() <= 0) return DG_ERR_NO_DEVICE;
-  context_plan_kernel<<<kPlanCtas, kPlanThreads, 0, static_cast<cudaStream_t>(stream)>>>(*ctx, add, release, commit);
-  return cuda_ok(cudaGetLastError(), "context plan launch") ? DG_OK : DG_ERR_CUDA;
+  return cuda_ok(launch_context(context_plan_kernel, dim3(kPlanCtas), kPlanThreads, 0, static_cast<cudaStream_t>(stream),
+                                *ctx, add, release, commit),
+                 "context plan launch")
+             ? DG_OK
+             : DG_ERR_CUDA;
 }
 
 dg_status dg_context_status(const dg_context* ctx, void* stream) {
@@ -542,18 +695,18 @@ dg_status dg_rope(const dg_heads* x, const dg_heads* out, int32_t rows, int32_t 
   if (sms <= 0) return DG_ERR_NO_DEVICE;
   if (rows == 0) return DG_OK;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  const int stride = kRopeThreads / (dim / 16);
   auto launch = [&](auto kernel, int tokens) {
-    kernel<<<(rows + tokens - 1) / tokens, kRopeThreads, 0, cs>>>(
-        static_cast<const uint8_t*>(x->data), static_cast<uint8_t*>(out->data), x->row_stride, x->head_stride,
-        out->row_stride, out->head_stride, rows, heads, dim, positions, rope->freq, rope->rot, rope->interleaved,
-        rope->magnitude);
+    return launch_context(kernel, dim3((rows + tokens - 1) / tokens), kRopeThreads, 0, cs,
+                          static_cast<const uint8_t*>(x->data), static_cast<uint8_t*>(out->data), x->row_stride,
+                          x->head_stride, out->row_stride, out->head_stride, rows, heads, stride / heads,
+                          stride % heads, positions, rope->freq, rope->rot, rope->interleaved, rope->magnitude);
   };
   // few rows: a CTA per row, for the latency; else four, for the turns
-  if (rows <= 4 * sms)
-    launch(rope_kernel<1>, 1);
-  else
-    launch(rope_kernel<4>, 4);
-  return cuda_ok(cudaGetLastError(), "rope launch") ? DG_OK : DG_ERR_CUDA;
+  const bool few = rows <= 4 * sms;
+  const cudaError_t e = dim == 128 ? (few ? launch(rope_kernel<128, 1>, 1) : launch(rope_kernel<128, 4>, 4))
+                                   : (few ? launch(rope_kernel<64, 1>, 1) : launch(rope_kernel<64, 4>, 4));
+  return cuda_ok(e, "rope launch") ? DG_OK : DG_ERR_CUDA;
 }
 
 dg_status dg_context_append(const dg_context* ctx, const dg_context_cache* cache, const dg_heads* k,
@@ -563,13 +716,20 @@ dg_status dg_context_append(const dg_context* ctx, const dg_context_cache* cache
   if ((st = check_heads(k, cache->heads, cache->dim)) != DG_OK) return st;
   if ((st = check_heads(v, cache->heads, cache->dim)) != DG_OK) return st;
   if (rope != nullptr && (st = check_rope(rope, cache->dim)) != DG_OK) return st;
-  if (device_sms() <= 0) return DG_ERR_NO_DEVICE;
-  const dim3 grid(DG_CONTEXT_RUNS(ctx->rows, ctx->B), cache->heads, 2);
+  const int sms = device_sms();
+  if (sms <= 0) return DG_ERR_NO_DEVICE;
   const dg_rope_args none = {};
-  auto kernel = cache->dim == 128 ? context_append_kernel<128> : context_append_kernel<64>;
-  kernel<<<grid, kAppendThreads, 0, static_cast<cudaStream_t>(stream)>>>(*ctx, *cache, *k, *v, rope ? *rope : none,
-                                                                         rope != nullptr);
-  return cuda_ok(cudaGetLastError(), "context append launch") ? DG_OK : DG_ERR_CUDA;
+  // a batch has about a run per page's worth of rows and one per request;
+  // three or four CTAs share an SM
+  const int64_t runs = ctx->rows / DG_PAGE + ctx->B;
+  int per = 1;
+  while (per < cache->heads && 2 * runs * ((cache->heads + per - 1) / per) > 4 * static_cast<int64_t>(sms)) per *= 2;
+  const dim3 grid(DG_CONTEXT_RUNS(ctx->rows, ctx->B), (cache->heads + per - 1) / per, 2);
+  auto kernel = cache->dim == 128 ? (per > 1 ? context_append_kernel<128, true> : context_append_kernel<128, false>)
+                                  : (per > 1 ? context_append_kernel<64, true> : context_append_kernel<64, false>);
+  const cudaError_t e = launch_context(kernel, grid, cache->dim * (DG_PAGE / 16) / kMine, 0, static_cast<cudaStream_t>(stream),
+                                       *ctx, *cache, *k, *v, rope ? *rope : none, rope != nullptr, per);
+  return cuda_ok(e, "context append launch") ? DG_OK : DG_ERR_CUDA;
 }
 
 }  // extern "C"

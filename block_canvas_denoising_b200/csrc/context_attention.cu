@@ -117,6 +117,8 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     mbar_init(smem_u32(&s_bars[warp][1]), 1);
     fence_mbarrier_init();
   }
+  wait_for_previous_kernel();
+  allow_next_kernel();
   S::totals(p, s_before);
   const int64_t total = s_before[p.B];
   const int64_t even = (total + gridDim.x - 1) / gridDim.x;
@@ -574,10 +576,10 @@ template <int kDim>
 cudaError_t launch_rows(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& p, bool eight, const AttnWs& ws,
                         cudaStream_t stream) {
   if (eight)
-    attention_rows_kernel<kDim, 1><<<ws.grid8, RowsCfg<kDim, 1>::kThreads, RowsCfg<kDim, 1>::kSmem, stream>>>(tmK, tmV, p);
-  else
-    attention_rows_kernel<kDim, 2><<<ws.grid16, RowsCfg<kDim, 2>::kThreads, RowsCfg<kDim, 2>::kSmem, stream>>>(tmK, tmV, p);
-  return cudaGetLastError();
+    return launch_context(attention_rows_kernel<kDim, 1>, dim3(ws.grid8), RowsCfg<kDim, 1>::kThreads,
+                          RowsCfg<kDim, 1>::kSmem, stream, tmK, tmV, p);
+  return launch_context(attention_rows_kernel<kDim, 2>, dim3(ws.grid16), RowsCfg<kDim, 2>::kThreads,
+                        RowsCfg<kDim, 2>::kSmem, stream, tmK, tmV, p);
 }
 
 bool shape_ok(int64_t rows, int64_t q_heads, int64_t kv_heads, int dim) {

@@ -19,6 +19,7 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include "context.h"
 #include "context_attention.h"
 #include "dg_internal.h"
 #include "per_device.h"
@@ -450,12 +451,13 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     tmem_alloc1(smem_u32(&sh.tmem), 512);
     tmem_relinquish1();
   }
+  wait_for_previous_kernel();
+  allow_next_kernel();
   S::totals(p, sh.before);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh.tmem;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // the joining kernel may take its place
   // columns: S (and P over it) of group g, buffer b at 128 g + 64 b, O at 256 + 128 g
   const int64_t total = sh.before[p.B];
   const int64_t even = (total + gridDim.x - 1) / gridDim.x;
@@ -919,7 +921,8 @@ constexpr int kJoinThreads = 256;
 template <int kDim>
 __global__ void __launch_bounds__(kJoinThreads)
 attention_join_kernel(const __grid_constant__ AttnParams p) {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  wait_for_previous_kernel();
+  allow_next_kernel();
   constexpr int kPartFloats = TilesCfg<kDim>::kPartFloats;
   const Piece w = static_cast<const Piece*>(p.splits)[blockIdx.x];
   if (w.parts < 2) return;
@@ -1007,19 +1010,9 @@ size_t tiles_split_bytes() { return sizeof(Piece); }
 namespace {
 template <int kDim>
 cudaError_t launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& p, int grid, cudaStream_t stream) {
-  attention_tiles_kernel<kDim><<<grid, kTilesThreads, TilesCfg<kDim>::kSmem, stream>>>(tmK, tmV, p);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_context(attention_tiles_kernel<kDim>, dim3(grid), kTilesThreads, TilesCfg<kDim>::kSmem, stream, tmK, tmV, p);
   if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid, kDim / 16);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attention_join_kernel<kDim>, p);
+  return launch_context(attention_join_kernel<kDim>, dim3(grid, kDim / 16), kJoinThreads, 0, stream, p);
 }
 }  // namespace
 

@@ -137,6 +137,12 @@ DG_DEV void tma_load_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int 
 // asynchronous proxy (TMA, tcgen05 operands).
 DG_DEV void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+// Programmatic dependent launch: wait until the kernels before this one in
+// the stream have completed and their writes are visible (a no-op for an
+// ordinary launch); let the next kernel's blocks come up while this one ends.
+DG_DEV void wait_for_previous_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+DG_DEV void allow_next_kernel() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // clusters
 // ---------------------------------------------------------------------------
