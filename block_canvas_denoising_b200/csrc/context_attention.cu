@@ -548,7 +548,10 @@ int rows_grid() {
 }
 
 // Workspace: the fault latch, the tickets, the split items, the parts.  Sized
-// for all kernels, so that one workspace serves every batch of a shape.
+// for all kernels, so that one workspace serves every batch of a shape; the
+// tickets' place, which has to stay zero between calls, is the same for every
+// shape.
+constexpr int kMaxGrid = 1024;
 struct AttnWs {
   int grid8, grid16, tiles_grid;  // resident CTAs of the rows kernels and of the tiles kernel
   size_t tickets, splits, part, total;
@@ -559,14 +562,14 @@ bool attn_ws(AttnWs* w) {
   w->grid16 = rows_grid<kDim, 2>();
   w->tiles_grid = tiles_grid(kDim);
   if (w->grid8 < 1 || w->grid16 < 1 || w->tiles_grid < 1) return false;
+  if (w->grid8 > kMaxGrid || w->grid16 > kMaxGrid || w->tiles_grid > kMaxGrid) return false;
   auto up = [](size_t n) { return (n + kWsAlign - 1) / kWsAlign * kWsAlign; };
   auto most = [](size_t a, size_t b) { return a > b ? a : b; };
-  const size_t grid = most(w->grid8, most(w->grid16, w->tiles_grid));
   const size_t floats = most(w->grid8 * size_t(RowsCfg<kDim, 1>::kPartFloats),
                              most(w->grid16 * size_t(RowsCfg<kDim, 2>::kPartFloats), w->tiles_grid * tiles_part_floats(kDim)));
   w->tickets = kWsAlign;
-  w->splits = w->tickets + up(grid * 4);
-  w->part = w->splits + up(grid * tiles_split_bytes());
+  w->splits = w->tickets + up(kMaxGrid * 4);
+  w->part = w->splits + up(kMaxGrid * tiles_split_bytes());
   w->total = w->part + 2 * sizeof(float) * floats;
   return true;
 }

@@ -472,7 +472,8 @@ dg_status dg_rope_frequencies(int32_t rot, double base, int32_t scaling, double 
 /* out = x rotated: x, out bf16 [rows][heads][dim], dim 64 or 128; out may be
  * x itself, and must not overlap it otherwise.  positions int32 [rows]
  * (device): a row whose position is negative is left alone.  Angles are
- * formed and reduced in float64, the rotation in float32, one rounding. */
+ * formed and reduced exactly as 64-bit fractions of a turn, from the float64
+ * frequency; the rotation is in float32, with one rounding at its end. */
 dg_status dg_rope(const dg_heads* x, const dg_heads* out, int32_t rows, int32_t heads, int32_t dim,
                   const int32_t* positions, const dg_rope_args* rope, void* stream);
 
@@ -500,7 +501,9 @@ dg_status dg_context_append(const dg_context* ctx, const dg_context_cache* cache
                             const dg_heads* v, const dg_rope_args* rope, void* stream);
 
 /* Workspace of dg_context_attention on the current device (0 if invalid),
- * zeroed once by dg_workspace_init(); its faults: dg_device_status(). */
+ * zeroed once by dg_workspace_init(); its faults: dg_device_status().  One
+ * workspace serves every call of its dim, one after another, whatever the
+ * batch; after a fault it is to be initialised again. */
 size_t dg_context_workspace_size(int32_t rows, int32_t q_heads, int32_t kv_heads, int32_t dim);
 
 /* dg_context_attention -- out = softmax(scale q . k) v of the batch's rows

@@ -611,3 +611,59 @@ def test_attention_under_load_equals_itself():
         torch.cuda.synchronize()
     for _, ws, _ in work:
         assert dg.device_status(ws) == 0
+
+
+def test_cache_beyond_32_bit_offsets():
+    # 70,000 pages of 8 heads x 64 x 128: 4.6 GB of codes each, the request's pages at the far end
+    rng = np.random.default_rng(17)
+    pages, kv, dim = 70000, 8, 128
+    cache = dg.ContextCache(pages, kv, dim)
+    small = dg.ContextCache(8, kv, dim)
+    for add, most in (([150], 0), ([2], 2)):
+        big, ref = dg.ContextPlan(1, 150, pages, 4), dg.ContextPlan(1, 150, 8, 4)
+        qkv = bf16(rng, 150, 3 * kv, dim)
+        outs = []
+        for plan, c in ((big, cache), (ref, small)):
+            dg.context_plan(plan, ints(add))  # pages come from the top of the stack
+            dg.context_append(plan, c, qkv[:, kv:2 * kv], qkv[:, 2 * kv:])
+            out = torch.zeros((150, kv, dim), dtype=torch.bfloat16, device="cuda")
+            dg.context_attention(plan, c, qkv[:, :kv], out, dg.ContextWorkspace(150, kv, kv, dim), max_new=most)
+            outs.append(out)
+        assert int(big.table[0, 0]) == pages - 1 and int(big.slots[0]) == (pages - 1) * 64
+        assert torch.equal(outs[0], outs[1]) and outs[0].abs().max() > 0
+
+
+def test_a_batch_without_rows():
+    rng = np.random.default_rng(18)
+    plan, cache, q = setup(rng, [10, 100], [5, 3], 4, 2, 128)
+    dg.context_plan(plan, ints([0, 0]))
+    assert plan.start.cpu().tolist() == [0, 0, 0] and (plan.positions == -1).all() and (plan.runs[:, 0] == -1).all()
+    before = cache.k.clone()
+    dg.context_append(plan, cache, q[:, :2], q[:, 2:])
+    assert torch.equal(before, cache.k)
+    for most in (0, 1):
+        check_attention(plan, cache, q, [1, 0], max_new=most)
+
+
+@pytest.mark.parametrize("B,heads,kv,dim", [(256, 3, 3, 64), (256, 2, 1, 128), (3, 64, 64, 64), (2, 99, 3, 128), (1, 320, 5, 64)])
+def test_attention_many_requests_and_heads(B, heads, kv, dim):
+    rng = np.random.default_rng(B + heads)
+    held = rng.integers(0, 150, B).tolist()
+    add = [1] * B
+    add[0] = 2
+    plan, cache, q = setup(rng, held, add, heads, kv, dim)
+    causal = rng.integers(0, 2, B).tolist()
+    check_attention(plan, cache, q, causal, max_new=2)
+    check_attention(plan, cache, q, causal, window=33)
+
+
+def test_one_workspace_for_many_shapes():
+    rng = np.random.default_rng(19)
+    ws = None
+    for dim, add, heads, kv in ((128, [1, 1], 8, 2), (64, [200, 3], 4, 1), (128, [3, 100], 4, 2), (64, [1, 1], 16, 1), (64, [2, 1], 4, 4)):
+        plan, cache, q = setup(rng, [2000, 50], add, heads, kv, dim)
+        if ws is None:
+            ws = dg.ContextWorkspace(plan.rows, heads, kv, dim)
+        elif dg.context_workspace_size(plan.rows, heads, kv, dim) > ws.nbytes:
+            continue
+        check_attention(plan, cache, q, [1, 0], ws=ws, max_new=max(add), rows_of=[0, 1, 2, 99, 199])

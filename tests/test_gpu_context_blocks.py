@@ -109,3 +109,39 @@ def test_a_pool_that_is_too_small_ends_the_generation():
                                    b["prev_argmax"], b["accept"], b["entropy"], b["sampled"], b["argmax"], b["stop"],
                                    dg.Workspace(B, D, V))
     assert err.value.code == 10 and set(seen) == {0}
+
+
+def test_context_ops_inside_the_device_loop():
+    # the hidden-state graph of the device loop runs a layer over the context
+    # every step; the last step's attention equals the same calls made eagerly
+    E_bits = synth.embedder_normal(V, D, seed=1)
+    E = to_dev_bf16(E_bits)
+    y = synth.loop_targets(L, V, seed=3, B=B)
+    table = torch.stack([to_dev_bf16(synth.loop_hidden(k, y, E_bits, seed=4)).reshape(-1) for k in range(48)])
+    heads, kv, dim = 4, 2, 64
+    plan = dg.ContextPlan(B, B * L, 40, 20)
+    cache = dg.ContextCache(plan.pages, kv, dim)
+    f = dg.RopeFrequencies(dim)
+    ws_a = dg.ContextWorkspace(plan.rows, heads, kv, dim)
+    out, q = (torch.zeros((B * L, heads, dim), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    dg.context_plan(plan, torch.full((B,), L, dtype=torch.int32, device="cuda"))
+    b = _buffers()
+
+    def layer(h, cache, out):
+        x = h.view(B * L, heads, dim)
+        dg.context_append(plan, cache, x[:, :kv], x[:, kv:], rope=f)
+        dg.rope(x, plan.positions, f, out=q)
+        dg.context_attention(plan, cache, q, out, ws_a, max_new=L)
+    state = dg.LoopState(B)
+    g = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(g):
+        b["h_buf"].view(-1).copy_(torch.index_select(table, 0, state.k.to(torch.int64).clamp(0, 47))[0])
+        layer(b["h_buf"], cache, out)
+    steps = dg.denoise_loop_graph(E, g, b["h_buf"], b["canvas"], b["prev_argmax"], np.zeros(B, np.uint8), b["accept"],
+                                  b["entropy"], b["sampled"], b["argmax"], b["stop"], dg.Workspace(B, D, V), state)
+    torch.cuda.synchronize()
+    last = int(steps.max()) - 1
+    again, cache2 = torch.zeros_like(out), dg.ContextCache(plan.pages, kv, dim)
+    layer(table[last].view(B * L, D), cache2, again)
+    assert torch.equal(out, again) and out.abs().max() > 0
+    assert dg.context_status(plan) == 0 and dg.device_status(ws_a) == 0
