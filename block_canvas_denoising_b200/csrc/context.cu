@@ -305,8 +305,10 @@ constexpr int kRopeThreads = 256;
 // they are formed once, by one thread per (token, frequency), and kept in
 // shared memory; the heads then stream through, 32 bytes a thread, a thread
 // staying on its unit and walking the (token, head) pairs by a fixed stride
-// (256 threads / units = step_tokens * heads + step_heads), without a division (with one per item the integer pipe was the bound: 14.6 us for
-// 8191 rows x 16 heads).
+// (256 threads / units = step_tokens * heads + step_heads) without a division.
+// Bound by memory: 67 MB of 8191 rows x 16 heads x 128 take 12.5 us on their
+// own, 5.4 TB/s (14.6 us with a division per item, which kept the integer pipe
+// busy).
 template <int kDim, int kTokens>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(const uint8_t* x, uint8_t* out, int64_t xr, int64_t xh, int64_t outr, int64_t outh, int rows, int heads,
@@ -420,23 +422,21 @@ DG_DEV uint2 e4m3_chunk(const float (&x)[8], float inv) {
 // all of their codes, so no two CTAs meet.  A thread has kMine units of 16
 // elements (a run of 64 rows fills the block); they stay in registers between
 // the two things that need them, the largest magnitude and the codes, and the
-// next head's are on their way meanwhile.  The turns of the run's tokens serve
-// all of its heads.  Many rows: as many heads a CTA as give one wave over the
-// device; few: one, for the latency, each thread forming its own turns.
+// next head's are on their way meanwhile.  The turns of the run's tokens are
+// formed once and serve all of its heads.
 constexpr int kMine = 2;
 template <int kDim>
 constexpr int kAppendThreads = DG_PAGE * kDim / 16 / kMine;
 
-template <int kDim, bool kShare>
+template <int kDim>
 __global__ void __launch_bounds__(kAppendThreads<kDim>)
 context_append_kernel(const dg_context c, const dg_context_cache cache, const dg_heads kin, const dg_heads vin,
                       const dg_rope_args rope, int has_rope, int per) {
   constexpr int kUnits = kDim / 16;  // units per row
   constexpr int kThreads = kAppendThreads<kDim>, kWarps = kThreads / 32;
   constexpr int kRows = kThreads / kUnits;        // rows between a thread's units
-  constexpr int kPairs = kShare ? kDim / 2 : 1;   // turns kept per token
   __shared__ float s_top[3][kWarps];
-  __shared__ __align__(16) float2 s_turn[kShare ? DG_PAGE : 1][kPairs];
+  __shared__ __align__(16) float2 s_turn[DG_PAGE][kDim / 2];
   wait_for_previous_kernel();
   allow_next_kernel();
   const int4 run = reinterpret_cast<const int4*>(c.runs)[blockIdx.x];
@@ -467,7 +467,7 @@ context_append_kernel(const dg_context c, const dg_context_cache cache, const dg
     }
   };
   load(src);
-  if (kShare && rot16 > 0) {
+  if (rot16 > 0) {
     const int half = 8 * rot16, stride = kThreads / half;
     const int j = threadIdx.x % half;  // this thread's frequency; the block's threads walk the rows
     const uint64_t turn = turn_fraction(rope.freq[j]);
@@ -491,13 +491,7 @@ context_append_kernel(const dg_context c, const dg_context_cache cache, const dg
       for (int m = 0; m < kMine; ++m) {
         if (row + m * kRows >= n) continue;
         float2 tr[8];
-        if (kShare) {
-          read_turns(s_turn[row + m * kRows], u, rot16, tr);
-        } else {
-          const uint32_t pos = c.positions[row0] + row + m * kRows;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) tr[j] = turn_of(pos * turn_fraction(rope.freq[8 * u + j]), rope.magnitude);
-        }
+        read_turns(s_turn[row + m * kRows], u, rot16, tr);
         rotate_unit(a[m], b[m], tr, il);
       }
     }
@@ -702,7 +696,9 @@ dg_status dg_rope(const dg_heads* x, const dg_heads* out, int32_t rows, int32_t 
                           x->head_stride, out->row_stride, out->head_stride, rows, heads, stride / heads,
                           stride % heads, positions, rope->freq, rope->rot, rope->interleaved, rope->magnitude);
   };
-  // few rows: a CTA per row, for the latency; else four, for the turns
+  // Few rows: a CTA per row, for the latency; else four, for fewer starts.  One
+  // / four rows a CTA, in us (22 heads x 128): 32 rows 1.9 / 2.5, 592 rows 2.5 /
+  // 2.7, 1184 rows 4.2 / 3.2; 8191 rows x 16 heads 18.9 / 10.9.
   const bool few = rows <= 4 * sms;
   const cudaError_t e = dim == 128 ? (few ? launch(rope_kernel<128, 1>, 1) : launch(rope_kernel<128, 4>, 4))
                                    : (few ? launch(rope_kernel<64, 1>, 1) : launch(rope_kernel<64, 4>, 4));
@@ -719,14 +715,15 @@ dg_status dg_context_append(const dg_context* ctx, const dg_context_cache* cache
   const int sms = device_sms();
   if (sms <= 0) return DG_ERR_NO_DEVICE;
   const dg_rope_args none = {};
-  // a batch has about a run per page's worth of rows and one per request;
-  // three or four CTAs share an SM
-  const int64_t runs = ctx->rows / DG_PAGE + ctx->B;
+  // More heads a CTA save turns and starts, until too few CTAs are left to
+  // fill the device: up to 3.5 an SM.  1 / 2 / 4 / 8 heads a CTA, in us (8 heads
+  // x 128): 32 requests x 1 row 4.5 / 3.6 / 4.4 / 5.6; 4 x 256 rows 4.5 / 5.2 /
+  // 5.4 / 8.0; 16 x 256 11.8 / 9.3 / 8.3 / 10.7; 32 x 256 19.9 / 14.8 / 12.8 / 12.2.
+  const int runs = DG_CONTEXT_RUNS(ctx->rows, ctx->B);
   int per = 1;
-  while (per < cache->heads && 2 * runs * ((cache->heads + per - 1) / per) > 4 * static_cast<int64_t>(sms)) per *= 2;
-  const dim3 grid(DG_CONTEXT_RUNS(ctx->rows, ctx->B), (cache->heads + per - 1) / per, 2);
-  auto kernel = cache->dim == 128 ? (per > 1 ? context_append_kernel<128, true> : context_append_kernel<128, false>)
-                                  : (per > 1 ? context_append_kernel<64, true> : context_append_kernel<64, false>);
+  while (per < cache->heads && 4ll * runs * ((cache->heads + per - 1) / per) > 7ll * sms) per *= 2;
+  const dim3 grid(runs, (cache->heads + per - 1) / per, 2);
+  auto kernel = cache->dim == 128 ? context_append_kernel<128> : context_append_kernel<64>;
   const cudaError_t e = launch_context(kernel, grid, cache->dim * (DG_PAGE / 16) / kMine, 0, static_cast<cudaStream_t>(stream),
                                        *ctx, *cache, *k, *v, rope ? *rope : none, rope != nullptr, per);
   return cuda_ok(e, "context append launch") ? DG_OK : DG_ERR_CUDA;
