@@ -669,13 +669,23 @@ dg_status dg_context_attention(const dg_context* ctx, const dg_context_cache* ca
   }
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   // Rows a kv head has in one request at most: the rows kernel takes 8 or 16
-  // at a time, the tiles kernel 256 whether they are there or not.
+  // at a time and reads the keys again for each, the tiles kernel takes 256
+  // whether they are there or not.  Microseconds of eights / sixteens / tiles:
+  //   rows                              8              16             32             48
+  //   32 requests x 5000 tokens     60  76 162    106  84 170    206 159 181    296 235 182
+  //   256 requests x 300 tokens     92 120 249    175 121 271    343 238 287    518 356 262
+  //   1 request x 4096 tokens       12  14  26     12  15  26     13  15  26     14  15  26
+  // (8 kv heads x 128; 4 in the last).  The lengths, which would tell the last
+  // row of these from the first, are on the device.
   const int64_t most = static_cast<int64_t>(max_new > 0 && max_new < ctx->rows ? max_new : ctx->rows) * p.group;
   cudaError_t e;
-  if (most > 16) {
+  if (most > 32) {
     p.min_tiles = 1;
     e = launch_attention_tiles(dim, tmK, tmV, p, ws.tiles_grid, cs);
   } else {
+    // A CTA that takes fewer pages than it has warps costs more in the joining
+    // than it saves: 1 / 4 / 8 / 16 / 32 pages at least take 16.0 / 15.0 / 11.9 /
+    // 12.7 / 15.1 us for one token over 4096 (4 kv heads x 128).
     p.min_tiles = 8;
     e = dim == 128 ? launch_rows<128>(tmK, tmV, p, most <= 8, ws, cs) : launch_rows<64>(tmK, tmV, p, most <= 8, ws, cs);
   }

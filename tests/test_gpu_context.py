@@ -285,6 +285,12 @@ def tokens(plan, cache, r, n):
     return got
 
 
+def value_scales(plan, cache, r):
+    """The scale of each token's values, [tokens of the pages, kv heads]."""
+    page = plan.table[r].cpu().numpy()[:-(-int(plan.lens[r]) // 64)]
+    return np.repeat(f64(cache.v_scale)[page], 64, axis=0)
+
+
 def check_attention(plan, cache, q, causal, window=0, scale=None, max_new=0, ws=None, rows_of=None):
     heads, dim = q.shape[1], cache.dim
     out = torch.full(q.shape, 3.0, dtype=torch.bfloat16, device="cuda")
@@ -313,9 +319,18 @@ def check_attention(plan, cache, q, causal, window=0, scale=None, max_new=0, ws=
             else:
                 lo = max(0, lens[r] - nq + i - window + 1) if window else 0
                 w, lw, mass, size = oc.attention(qs[i:i + 1], k[lo:], v[lo:], s, False, 0)
+            # Weights are at least 2^6 at the largest weight times page scale, in
+            # float16, whose smallest step is 2^-24: a weight further down is
+            # off by 2^-25, 2^-31 of the largest, however small the sum of
+            # weights times values is beside it (the largest weight's own value
+            # may be a 0).
+            first, last = (max(0, n - window) if window else 0, n) if c else (lo, n)
+            kk, vv, vs = (np.repeat(t[first:last], heads // cache.heads, axis=1) for t in (k, v, value_scales(plan, cache, r)[:n]))
+            share = np.exp(np.einsum("nhd,hd->nh", kk, qs[i]) * s - np.where(np.isinf(lw[0]), 0, lw[0])) * vs
+            tail = 2.0 ** -31 * share.max(0, initial=0)[:, None] * (np.abs(vv) / vs[..., None]).sum(0)
             terms = 2.0 ** -17 * s * np.abs(qs[i]).max(-1, keepdims=True) * np.abs(k).sum(-1).max(initial=0)
             d = (dim + 4) * 2.0 ** -24 * size[0][:, None] + terms
-            tol = 2.0 ** -8 * np.abs(w[0]) + (2.0 ** -11 + 2.0 ** -18 + 2 * d) * mass[0] + 1e-38
+            tol = 2.0 ** -8 * np.abs(w[0]) + (2.0 ** -11 + 2.0 ** -18 + 2 * d) * mass[0] + tail + 1e-38
             err = np.abs(o[start[r] + i] - w[0])
             assert np.all(err <= tol), (r, i, float((err / tol).max()))
             worst = max(worst, float((err / tol).max()))
@@ -667,3 +682,27 @@ def test_one_workspace_for_many_shapes():
         elif dg.context_workspace_size(plan.rows, heads, kv, dim) > ws.nbytes:
             continue
         check_attention(plan, cache, q, [1, 0], ws=ws, max_new=max(add), rows_of=[0, 1, 2, 99, 199])
+
+
+@pytest.mark.parametrize("group,new,dim", [(1, 9, 128), (8, 3, 64), (11, 2, 128), (5, 5, 64), (16, 2, 128), (31, 1, 64),
+                                           (32, 1, 128), (1, 32, 64), (1, 33, 128), (11, 3, 64), (33, 1, 128), (8, 4, 128)])
+def test_attention_some_rows(group, new, dim):
+    # between a handful of rows per kv head and a tile of them, where kernels change
+    rng = np.random.default_rng(100 * group + new)
+    plan, cache, q = setup(rng, [700, 0, 63], [new, 1, new], 2 * group, 2, dim, behind=2)
+    check_attention(plan, cache, q, [0, 1, 1], max_new=new)
+    check_attention(plan, cache, q, [1, 0, 0], window=65, max_new=new)
+
+
+@pytest.mark.parametrize("B,heads,dim", [(40, 8, 128), (256, 8, 64), (40, 7, 64), (200, 5, 128)])
+def test_append_many_runs(B, heads, dim):
+    # so many pages are touched that a block takes several heads
+    rng = np.random.default_rng(B + heads)
+    held, add = rng.integers(0, 130, B).tolist(), rng.integers(0, 4, B).tolist()
+    plan = make_plan(rng, held, 3 * B, 3, sum(add) + 1)
+    dg.context_plan(plan, ints(add))
+    cache = random_cache(rng, plan.pages, heads, dim)
+    x = bf16(rng, plan.rows, 2 * heads, dim)
+    check_append(plan, cache, x[:, :heads], x[:, heads:])
+    f, mag = oc.frequencies(dim)
+    check_append(plan, cache, x[:, heads:], x[:, :heads], (f, mag, False), dg.RopeFrequencies(dim))
