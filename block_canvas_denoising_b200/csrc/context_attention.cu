@@ -121,7 +121,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
   allow_next_kernel();
   S::totals(p, s_before);
   const int64_t total = s_before[p.B];
-  const int64_t even = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t even = quotient(total + gridDim.x - 1, gridDim.x);
   const int64_t per = even > p.min_tiles ? even : p.min_tiles;
   int64_t pos = blockIdx.x * per;
   const int64_t end = min(pos + per, total);
@@ -425,7 +425,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     __syncthreads();
 
     const bool whole = pos == it.begin && item_end <= end;
-    const int c0 = static_cast<int>(it.begin / per), parts = static_cast<int>((item_end - 1) / per) - c0 + 1;
+    const int c0 = static_cast<int>(quotient(it.begin, per)), parts = static_cast<int>(quotient(item_end - 1, per)) - c0 + 1;
     float* part = p.part + static_cast<size_t>(2 * blockIdx.x + (static_cast<int>(blockIdx.x) == c0 ? 1 : 0)) * Cfg::kPartFloats;
     constexpr int kChunks = kM * kDim / 8;
     auto store = [&](int row, int d0, const float (&x)[8], float top, float sum) {

@@ -62,6 +62,12 @@ DG_DEV int key_lo(const AttnParams& p, const Request& q, int i) {
 }
 DG_DEV int key_hi(const Request& q, int i) { return q.causal ? q.len - q.nq + i : q.len - 1; }
 
+// a / b of numbers that are not negative; 64-bit division, a routine of some
+// hundred instructions, only where it takes 64 bits.
+DG_DEV int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? static_cast<int64_t>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+
 // Work is cut into tiles: kM packed query rows (row rho is query row rho /
 // group, head rho % group of the kv head) by kKeys keys.  An item is one
 // (request, row tile, kv head) with all key tiles that some row of it sees
@@ -79,9 +85,9 @@ struct Split {
     return static_cast<int>((static_cast<int64_t>(q.nq) * p.group + kM - 1) / kM);
   }
   static DG_DEV int item_tiles(const AttnParams& p, const Request& q, int mt, int* first) {
-    const int64_t rho = static_cast<int64_t>(mt) * kM;
-    const int i0 = static_cast<int>(rho / p.group);
-    const int i1 = min(static_cast<int>((rho + kM - 1) / p.group), q.nq - 1);
+    const uint32_t rho = static_cast<uint32_t>(mt) * kM, group = static_cast<uint32_t>(p.group);  // rows * group is below 2^31
+    const int i0 = static_cast<int>(rho / group);
+    const int i1 = min(static_cast<int>((rho + kM - 1) / group), q.nq - 1);
     const int lo = key_lo(p, q, i0), hi = key_hi(q, i1);
     *first = hi >= lo ? lo / kKeys : 0;
     return hi >= lo ? hi / kKeys - lo / kKeys + 1 : 1;
@@ -162,9 +168,9 @@ struct Split {
     begin = before[r];
     if (!q.causal && p.window == 0) {  // every row tile sees the same keys
       tiles = item_tiles(p, q, 0, &first);
-      const int64_t n = (pos - begin) / (tiles + kCost);
-      mt = static_cast<int>(n / p.kv_heads);
-      h = static_cast<int>(n % p.kv_heads);
+      const int64_t n = quotient(pos - begin, tiles + kCost);
+      mt = static_cast<int>(quotient(n, p.kv_heads));
+      h = static_cast<int>(n - static_cast<int64_t>(mt) * p.kv_heads);
       begin += n * (tiles + kCost) + kCost;
       return;
     }
@@ -189,7 +195,7 @@ struct Split {
       first = __shfl_sync(0xffffffffu, f, at);
       begin += __shfl_sync(0xffffffffu, upto, at) - static_cast<int64_t>(units) * p.kv_heads;
       mt = m0 + at;
-      h = static_cast<int>((pos - begin) / units);
+      h = static_cast<int>(quotient(pos - begin, units));
       begin += static_cast<int64_t>(h) * units + kCost;
       tiles = units - kCost;
       return;

@@ -235,8 +235,21 @@ __host__ __device__ constexpr uint32_t idesc_f16_bmn(int M, int N) {
   return (1u << 4) | (1u << 16) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
 }
 
-DG_DEV uint32_t f2_to_e4m3x2(float lo, float hi) {
-  return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+// Two float16 to E4M3, to nearest even, saturating.
+DG_DEV uint32_t half2_to_e4m3x2(uint32_t v) {
+  uint32_t d;
+  asm("{\n\t.reg .b16 t;\n\tcvt.rn.satfinite.e4m3x2.f16x2 t, %1;\n\tcvt.u32.u16 %0, t;\n\t}" : "=r"(d) : "r"(v));
+  return d;
+}
+DG_DEV uint32_t sub_half2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+DG_DEV uint32_t max_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
 }
 DG_DEV uint32_t e4m3x2_to_half2(uint32_t w) {  // low 16 bits
   uint32_t d;
@@ -344,67 +357,81 @@ DG_DEV float prepare_q(const AttnParams& p, const Piece& w, uint32_t rho0, uint8
   constexpr int kLanes = kDim / 8;           // lanes per row
   constexpr int kAtOnce = 32 / kLanes;       // rows per step
   const int lane = threadIdx.x & 31, sub = lane / kLanes, c = lane % kLanes;
-  // chunk i of a row: the first dim / 16 lie in q1, the others in q2
+  // chunk i of a row: the first dim / 16 lie in q1, the others in q2 (a copied
+  // line of 128 bytes stays one: with chunks in q1 and q2 by turns the copies
+  // took twice as long)
   auto place = [&](int row, int i) {
     const int k = i & (kDim / 16 - 1);
     return (i < kDim / 16 ? q1 : q2) + (kDim == 128 ? row * 128 + ((k ^ (row & 7)) << 4) : row * 64 + ((k ^ ((row >> 1) & 3)) << 4));
   };
+  // this lane's first row, and the steps to its next ones, without a division
   const uint32_t group = static_cast<uint32_t>(p.group);
   uint32_t i = (rho0 + sub) / group, g = rho0 + sub - i * group;  // query row and head within the kv head
-  const uint8_t* base = p.q + w.row0 * p.q_row + static_cast<int64_t>(w.h) * group * p.q_head + 16 * c;
-#pragma unroll 4
+  const uint8_t* src = p.q + (w.row0 + i) * p.q_row + (static_cast<int64_t>(w.h) * group + g) * p.q_head + 16 * c;
+  const uint32_t step_i = kAtOnce / group, step_g = kAtOnce - step_i * group;
+  const int64_t step = step_i * p.q_row + step_g * p.q_head, turn = p.q_row - group * p.q_head;
+#pragma unroll
   for (int k = 0; k < 32 / kAtOnce; ++k) {
-    const bool live = static_cast<int>(i) < w.nq;
-    const uint8_t* src = live ? base + i * p.q_row + g * p.q_head : base;
     // a row that is not there: nothing is read and the place is filled with zeros
+    const bool live = static_cast<int>(i) < w.nq;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(place(row0 + k * kAtOnce + sub, c))),
-                 "l"(src), "r"(live ? 16 : 0)
+                 "l"(live ? src : p.q), "r"(live ? 16 : 0)
                  : "memory");
-    for (g += kAtOnce; g >= group; g -= group) ++i;
+    i += step_i;
+    g += step_g;
+    src += step;
+    if (g >= group) {
+      g -= group;
+      ++i;
+      src += turn;
+    }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
   __syncwarp();
   const int row = row0 + lane;
-  uint32_t top = 0;  // the largest magnitude: float32 bits of the bf16 halves, as integers
+  // The largest magnitude, two bf16 at a time (a NaN passes through): its
+  // exponent, all ones if something is not finite.
+  uint32_t most = 0;
 #pragma unroll
   for (int i = 0; i < kDim / 8; ++i) {
     const uint4 v = *reinterpret_cast<const uint4*>(place(row, i));
-    const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) top = max(max(top, (u[j] << 16) & 0x7FFFFFFFu), u[j] & 0x7FFF0000u);
+    most = max_bf16x2(max_bf16x2(most, max_bf16x2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu)),
+                      max_bf16x2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
   }
+  const uint32_t top = max(most << 16, most & 0xFFFF0000u);  // float32 bits
   const int b = static_cast<int>(top >> 23);
   const int e = b == 0 ? 0 : min(7 - (b - 127), 120);  // largest magnitude to [2^7, 2^8)
   const bool finite = b < 255;
   const float f = pow2i(e);
-  // Chunks 2i and 2i + 1 become chunk i of both terms.  The first term's
-  // place is chunk i, which has been read by then; the second's is not, and
-  // waits in registers.
-  uint4 second[kDim / 16];
-#pragma unroll
-  for (int i = 0; i < kDim / 16; ++i) {
+  // Chunks 2i and 2i + 1 become chunk i of both terms, in an order in which
+  // every place has been read before it is written; a quarter of the row waits
+  // in registers.
+  auto terms = [&](int i, const uint4& v0, const uint4& v1) {
+    const uint32_t u[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
     uint32_t t1[4], t2[4];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const uint4 v = *reinterpret_cast<const uint4*>(place(row, 2 * i + h));
-      const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const float x[4] = {__uint_as_float(u[2 * j] << 16) * f, __uint_as_float(u[2 * j] & 0xFFFF0000u) * f,
-                            __uint_as_float(u[2 * j + 1] << 16) * f, __uint_as_float(u[2 * j + 1] & 0xFFFF0000u) * f};
-        const uint32_t lo = f2_to_e4m3x2(x[0], x[1]), hi = f2_to_e4m3x2(x[2], x[3]);
-        const uint32_t hl = e4m3x2_to_half2(lo), hh = e4m3x2_to_half2(hi);
-        const float2 bl = __half22float2(*reinterpret_cast<const __half2*>(&hl));
-        const float2 bh = __half22float2(*reinterpret_cast<const __half2*>(&hh));
-        t1[2 * h + j] = finite ? (lo | hi << 16) : 0x7F7F7F7Fu;  // a row that is not finite: NaN throughout
-        t2[2 * h + j] = f2_to_e4m3x2(x[0] - bl.x, x[1] - bl.y) | f2_to_e4m3x2(x[2] - bh.x, x[3] - bh.y) << 16;
-      }
+    for (int j = 0; j < 4; ++j) {
+      // float16 holds the scaled values to 2^-25, far below what the terms do
+      const uint32_t x0 = pack_half2(__uint_as_float(u[2 * j] << 16) * f, __uint_as_float(u[2 * j] & 0xFFFF0000u) * f);
+      const uint32_t x1 = pack_half2(__uint_as_float(u[2 * j + 1] << 16) * f, __uint_as_float(u[2 * j + 1] & 0xFFFF0000u) * f);
+      const uint32_t lo = half2_to_e4m3x2(x0), hi = half2_to_e4m3x2(x1);
+      t1[j] = finite ? (lo | hi << 16) : 0x7F7F7F7Fu;  // a row that is not finite: NaN throughout
+      t2[j] = half2_to_e4m3x2(sub_half2(x0, e4m3x2_to_half2(lo))) | half2_to_e4m3x2(sub_half2(x1, e4m3x2_to_half2(hi))) << 16;
     }
     *reinterpret_cast<uint4*>(place(row, i)) = make_uint4(t1[0], t1[1], t1[2], t1[3]);
-    second[i] = make_uint4(t2[0], t2[1], t2[2], t2[3]);
-  }
+    *reinterpret_cast<uint4*>(place(row, kDim / 16 + i)) = make_uint4(t2[0], t2[1], t2[2], t2[3]);
+  };
+  auto chunk = [&](int i) { return *reinterpret_cast<const uint4*>(place(row, i)); };
+  constexpr int kH = kDim / 32;
+  uint4 kept[kH];  // chunks kH .. 2 kH - 1
 #pragma unroll
-  for (int i = 0; i < kDim / 16; ++i) *reinterpret_cast<uint4*>(place(row, kDim / 16 + i)) = second[i];
+  for (int j = 0; j < kH; ++j) kept[j] = chunk(kH + j);
+#pragma unroll 2
+  for (int i = 2 * kH - 1; i >= kH; --i) terms(i, chunk(2 * i), chunk(2 * i + 1));
+#pragma unroll
+  for (int i = 0; i < kH / 2; ++i) terms(i, chunk(2 * i), chunk(2 * i + 1));
+#pragma unroll
+  for (int i = kH / 2; i < kH; ++i) terms(i, kept[2 * i - kH], kept[2 * i + 1 - kH]);
   return finite ? p.scale_log2 * pow2i(-e) : 1.f;
 }
 
@@ -460,7 +487,7 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
   const uint32_t tmem = sh.tmem;
   // columns: S (and P over it) of group g, buffer b at 128 g + 64 b, O at 256 + 128 g
   const int64_t total = sh.before[p.B];
-  const int64_t even = (total + gridDim.x - 1) / gridDim.x;
+  const int64_t even = quotient(total + gridDim.x - 1, gridDim.x);
   const int64_t per = even > p.min_tiles ? even : p.min_tiles;
 
   bool ok = true;
@@ -514,8 +541,8 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         w.tiles = static_cast<int>(min(item_end, end) - pos);
         w.groups = static_cast<int64_t>(it.q.nq) * p.group - static_cast<int64_t>(it.mt) * kTilesM > kGroupRows ? 2 : 1;
         w.whole = w.tiles == it.tiles;
-        w.c0 = static_cast<int>(it.begin / per);
-        w.parts = static_cast<int>((item_end - 1) / per) - w.c0 + 1;
+        w.c0 = static_cast<int>(quotient(it.begin, per));
+        w.parts = static_cast<int>(quotient(item_end - 1, per)) - w.c0 + 1;
         pos += w.tiles;
         if (!w.whole && w.c0 == static_cast<int>(blockIdx.x)) split = w;  // an item that begins here and ends elsewhere
       }
