@@ -488,31 +488,35 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         auto part_of = [&](int i) {
           return p.part + static_cast<size_t>(2 * (c0 + i) + (i == 0 ? 1 : 0)) * Cfg::kPartFloats;
         };
+        constexpr int kAtOnce = 8;
         for (int c = threadIdx.x; c < kChunks; c += Cfg::kThreads) {
           const int row = c / (kDim / 8), d0 = (c % (kDim / 8)) * 8;
           float top = -FLT_MAX, sum = 0.f, x[8] = {};
-          for (int i0 = 0; i0 < parts; i0 += 4) {  // every read of four parts before the first use
-            float m4[4], l4[4];
-            float4 a4[4], b4[4];
+          for (int i0 = 0; i0 < parts; i0 += kAtOnce) {  // every read of some parts before the first use
+            float mi[kAtOnce], li[kAtOnce];
+            float4 ai[kAtOnce], bi[kAtOnce];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < kAtOnce; ++i) {
               const float* src = part_of(min(i0 + i, parts - 1));
-              m4[i] = __ldcg(src + kM * kDim + row);
-              l4[i] = __ldcg(src + kM * kDim + kM + row);
-              a4[i] = __ldcg(reinterpret_cast<const float4*>(src + row * kDim + d0));
-              b4[i] = __ldcg(reinterpret_cast<const float4*>(src + row * kDim + d0 + 4));
+              mi[i] = __ldcg(src + kM * kDim + row);
+              li[i] = __ldcg(src + kM * kDim + kM + row);
+              ai[i] = __ldcg(reinterpret_cast<const float4*>(src + row * kDim + d0));
+              bi[i] = __ldcg(reinterpret_cast<const float4*>(src + row * kDim + d0 + 4));
             }
+            float now = top;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if (i0 + i >= parts) break;
-              const float now = fmaxf(top, m4[i]);
-              const float old = join_weight(top, now), f = join_weight(m4[i], now);
-              top = now;
-              sum = sum * old + l4[i] * f;
-              x[0] = x[0] * old + a4[i].x * f; x[1] = x[1] * old + a4[i].y * f;
-              x[2] = x[2] * old + a4[i].z * f; x[3] = x[3] * old + a4[i].w * f;
-              x[4] = x[4] * old + b4[i].x * f; x[5] = x[5] * old + b4[i].y * f;
-              x[6] = x[6] * old + b4[i].z * f; x[7] = x[7] * old + b4[i].w * f;
+            for (int i = 0; i < kAtOnce; ++i) now = fmaxf(now, mi[i]);
+            const float old = join_weight(top, now);
+            top = now;
+            sum *= old;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= old;
+#pragma unroll
+            for (int i = 0; i < kAtOnce; ++i) {
+              const float f = i0 + i < parts ? join_weight(mi[i], now) : 0.f;  // behind the last part: that one again
+              sum += li[i] * f;
+              x[0] += ai[i].x * f; x[1] += ai[i].y * f; x[2] += ai[i].z * f; x[3] += ai[i].w * f;
+              x[4] += bi[i].x * f; x[5] += bi[i].y * f; x[6] += bi[i].z * f; x[7] += bi[i].w * f;
             }
           }
           store(row, d0, x, top, sum);
