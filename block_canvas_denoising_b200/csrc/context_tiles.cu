@@ -941,10 +941,14 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
 // Joins the parts of the items that more than one CTA worked on, in split
 // order, so results do not depend on which CTA was done first.  Block (c, y)
 // works on the item that begins in CTA c's range and ends behind it, if there
-// is one; a warp on 32 rows x 16 elements, 4 reads of 16 bytes a lane and
-// part, four parts at once: for one canvas, 22 items in 7 parts of 133 KB each,
-// spread over the whole device (one CTA joining an item alone took 32 us).
+// is one; a warp on 32 rows x 8 elements, every read of eight parts before the
+// first use.  For one canvas, 22 items in 7 parts of 133 KB each, spread over
+// the whole device, it is the latency that counts: with 16 elements and four
+// parts at once the canvas takes 34.8 instead of 33.1 us, while 32 canvases,
+// whose items have two parts, take 381 instead of 383 (one CTA joining an item
+// alone took 32 us).
 constexpr int kJoinThreads = 256;
+constexpr int kJoinParts = 8, kJoinVec = 2;  // parts at once, float4 of each
 template <int kDim>
 __global__ void __launch_bounds__(kJoinThreads)
 attention_join_kernel(const __grid_constant__ AttnParams p) {
@@ -954,37 +958,39 @@ attention_join_kernel(const __grid_constant__ AttnParams p) {
   const Piece w = static_cast<const Piece*>(p.splits)[blockIdx.x];
   if (w.parts < 2) return;
   const int unit = blockIdx.y * (kJoinThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  const int row = (unit & 7) * 32 + lane, c = unit >> 3;  // 16 elements from 16 c
-  if (c >= kDim / 16) return;
+  const int row = (unit & 7) * 32 + lane, c = unit >> 3;  // elements from 4 kJoinVec c
+  if (c >= kDim / (4 * kJoinVec)) return;
   const Row o = row_of(p, w, row);
   if (!o.live) return;
   auto part_of = [&](int i) { return p.part + static_cast<size_t>(2 * (w.c0 + i) + (i == 0 ? 1 : 0)) * kPartFloats; };
-  float top = -FLT_MAX, sum = 0.f, x[16] = {};
-  for (int i0 = 0; i0 < w.parts; i0 += 4) {  // every read of four parts before the first use
-    float m[4], l[4];
-    float4 v[4][4];
+  float top = -FLT_MAX, sum = 0.f, x[4 * kJoinVec] = {};
+  for (int i0 = 0; i0 < w.parts; i0 += kJoinParts) {  // every read of some parts before the first use
+    float m[kJoinParts], l[kJoinParts];
+    float4 v[kJoinParts][kJoinVec];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kJoinParts; ++i) {
       const float* src = part_of(min(i0 + i, w.parts - 1));
       m[i] = i0 + i < w.parts ? __ldcg(src + kTilesM * kDim + row) : -FLT_MAX;
       l[i] = i0 + i < w.parts ? __ldcg(src + kTilesM * kDim + kTilesM + row) : 0.f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
-        v[i][k] = i0 + i < w.parts ? __ldcg(reinterpret_cast<const float4*>(src) + (4 * c + k) * kTilesM + row)
+      for (int k = 0; k < kJoinVec; ++k)
+        v[i][k] = i0 + i < w.parts ? __ldcg(reinterpret_cast<const float4*>(src) + (kJoinVec * c + k) * kTilesM + row)
                                    : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    const float now = fmaxf(fmaxf(top, fmaxf(m[0], m[1])), fmaxf(m[2], m[3]));
+    float now = top;
+#pragma unroll
+    for (int i = 0; i < kJoinParts; ++i) now = fmaxf(now, m[i]);
     const float old = join_weight(top, now);
     top = now;
     sum *= old;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) x[k] *= old;
+    for (int k = 0; k < 4 * kJoinVec; ++k) x[k] *= old;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kJoinParts; ++i) {
       const float f = join_weight(m[i], top);
       sum += l[i] * f;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < kJoinVec; ++k) {
         x[4 * k] += v[i][k].x * f;
         x[4 * k + 1] += v[i][k].y * f;
         x[4 * k + 2] += v[i][k].z * f;
@@ -993,15 +999,15 @@ attention_join_kernel(const __grid_constant__ AttnParams p) {
     }
   }
   const float inv = saw_nothing(top, sum) ? 0.f : 1.0f / sum;
-  uint32_t b[8];
+  uint32_t b[2 * kJoinVec];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < 2 * kJoinVec; ++i) {
     const __nv_bfloat162 v = __floats2bfloat162_rn(x[2 * i] * inv, x[2 * i + 1] * inv);
     b[i] = *reinterpret_cast<const uint32_t*>(&v);
   }
-  uint4* dst = reinterpret_cast<uint4*>(p.out + o.token * p.out_row + o.head * p.out_head + 32 * c);
-  dst[0] = make_uint4(b[0], b[1], b[2], b[3]);
-  dst[1] = make_uint4(b[4], b[5], b[6], b[7]);
+  uint4* dst = reinterpret_cast<uint4*>(p.out + o.token * p.out_row + o.head * p.out_head + 8 * kJoinVec * c);
+#pragma unroll
+  for (int k = 0; k < kJoinVec / 2; ++k) dst[k] = make_uint4(b[4 * k], b[4 * k + 1], b[4 * k + 2], b[4 * k + 3]);
   if (p.lse != nullptr && c == 0)
     p.lse[o.token * (static_cast<int64_t>(p.kv_heads) * p.group) + o.head] =
         saw_nothing(top, sum) ? -INFINITY : (top - kWeightLog2 + log2f(sum)) * kLn2;
@@ -1039,7 +1045,7 @@ template <int kDim>
 cudaError_t launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const AttnParams& p, int grid, cudaStream_t stream) {
   const cudaError_t e = launch_context(attention_tiles_kernel<kDim>, dim3(grid), kTilesThreads, TilesCfg<kDim>::kSmem, stream, tmK, tmV, p);
   if (e != cudaSuccess) return e;
-  return launch_context(attention_join_kernel<kDim>, dim3(grid, kDim / 16), kJoinThreads, 0, stream, p);
+  return launch_context(attention_join_kernel<kDim>, dim3(grid, kDim / (4 * kJoinVec)), kJoinThreads, 0, stream, p);
 }
 }  // namespace
 
