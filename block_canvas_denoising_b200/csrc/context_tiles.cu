@@ -15,7 +15,7 @@
 //               widened to float16 (exact) by four warps of their own.
 // The running maximum only moves when it is exceeded by more than 2^8, so
 // O is seldom rescaled; weights stay below 2^(kWeightLog2 + 8) = 2^14.
-// Measured (22 heads over 2 kv heads x 128): 32 canvases of 256 rows over 2560
+// Measured (22 heads over 2 kv heads x 128): 32 canvases of 256 rows over 2816
 // to 5376 tokens in 380 us, 960 TFLOP/s at 1.9 GHz (under a sustained load, at
 // the power limit, 413 us), a canvas over 4352 in 33 us; 16 heads over 4, a canvas
 // at the end of 131072 tokens, in 264 us, 1.04 PFLOP/s.  A tile takes some

@@ -520,7 +520,7 @@ size_t dg_context_workspace_size(int32_t rows, int32_t q_heads, int32_t kv_heads
  *            it (0: not known): chooses the kernel, never the result's
  *            meaning.
  *   lse      float [rows][q_heads] or NULL: ln of the sum of exp(logits).
- * A row that sees no token gives 0 (lse -inf).  A query that is not finite
+ * Logits and sums are float32.  A row that sees no token gives 0 (lse -inf).  A query that is not finite
  * gives NaN in its own row and head only.  Cache codes must not be NaN
  * (dg_context_append stores none); tokens on a page outside the pool are not
  * seen.  Rows from start[B] on are left as they were.  Results do not depend

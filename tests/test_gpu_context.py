@@ -706,3 +706,10 @@ def test_append_many_runs(B, heads, dim):
     check_append(plan, cache, x[:, :heads], x[:, heads:])
     f, mag = oc.frequencies(dim)
     check_append(plan, cache, x[:, heads:], x[:, :heads], (f, mag, False), dg.RopeFrequencies(dim))
+
+
+@pytest.mark.parametrize("heads,kv,dim", [(1024, 1, 64), (600, 2, 128), (1024, 1024, 64)])
+def test_attention_largest_groups(heads, kv, dim):
+    rng = np.random.default_rng(heads + kv)
+    plan, cache, q = setup(rng, [70, 0], [2, 1], heads, kv, dim, behind=1)
+    check_attention(plan, cache, q, [1, 0], max_new=2)
