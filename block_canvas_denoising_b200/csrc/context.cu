@@ -308,9 +308,8 @@ constexpr int kRopeThreads = 256;
 // shared memory; the heads then stream through, 32 bytes a thread, a thread
 // staying on its unit and walking the (token, head) pairs by a fixed stride
 // (256 threads / units = step_tokens * heads + step_heads) without a division.
-// Bound by memory: 67 MB of 8191 rows x 16 heads x 128 take 12.5 us on their
-// own, 5.4 TB/s (14.6 us with a division per item and float64 angles, which kept
-// the integer and the float64 pipe busy).
+// Bound by memory: 67 MB of 8191 rows x 16 heads x 128 take 13.1 us from HBM,
+// 5.1 TB/s, 0.78 of a plain copy's rate.
 template <int kDim, int kTokens>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(const uint8_t* x, uint8_t* out, int64_t xr, int64_t xh, int64_t outr, int64_t outh, int rows, int heads,
@@ -702,12 +701,20 @@ dg_status dg_rope(const dg_heads* x, const dg_heads* out, int32_t rows, int32_t 
                           x->head_stride, out->row_stride, out->head_stride, rows, heads, stride / heads,
                           stride % heads, positions, rope->freq, rope->rot, rope->interleaved, rope->magnitude);
   };
-  // Few rows: a CTA per row, for the latency; else four, for fewer starts.  One
-  // / four rows a CTA, in us (22 heads x 128): 32 rows 1.9 / 2.5, 592 rows 2.5 /
-  // 2.7, 1184 rows 4.2 / 3.2; 8191 rows x 16 heads 18.9 / 10.9.
-  const bool few = rows <= 4 * sms;
-  const cudaError_t e = dim == 128 ? (few ? launch(rope_kernel<128, 1>, 1) : launch(rope_kernel<128, 4>, 4))
-                                   : (few ? launch(rope_kernel<64, 1>, 1) : launch(rope_kernel<64, 4>, 4));
+  // Few rows: a CTA per row, for the latency; more: four or eight, for fewer
+  // starts and a longer stream per thread, 32 where a row is short.  In us, 22
+  // heads x 128 with 1 / 4 rows a CTA: 32 rows 1.9 / 2.5, 592 rows 2.5 / 2.7,
+  // 1184 rows 4.2 / 3.2.  With 4 / 8 (inputs from HBM): 2000 x 22 heads 5.2 / 5.7,
+  // 4000 x 16 8.2 / 7.6, 8191 x 16 14.2 / 13.1, 8191 x 32 23.3 / 23.9.  With 8 / 32:
+  // 16384 x 8 14.8 / 15.7, 32768 x 4 18.7 / 17.0, 131072 x 1 60 / 39.
+  const int64_t width = static_cast<int64_t>(heads) * dim;
+  const int tokens = rows <= 4 * sms ? 1 : (rows < 24 * sms || width >= 4096) ? 4 : width > 512 ? 8 : 32;
+  auto start = [&](auto one, auto four, auto eight, auto many) {
+    return tokens == 1 ? launch(one, 1) : tokens == 4 ? launch(four, 4) : tokens == 8 ? launch(eight, 8) : launch(many, 32);
+  };
+  const cudaError_t e =
+      dim == 128 ? start(rope_kernel<128, 1>, rope_kernel<128, 4>, rope_kernel<128, 8>, rope_kernel<128, 32>)
+                 : start(rope_kernel<64, 1>, rope_kernel<64, 4>, rope_kernel<64, 8>, rope_kernel<64, 32>);
   return cuda_ok(e, "rope launch") ? DG_OK : DG_ERR_CUDA;
 }
 

@@ -713,3 +713,26 @@ def test_attention_largest_groups(heads, kv, dim):
     rng = np.random.default_rng(heads + kv)
     plan, cache, q = setup(rng, [70, 0], [2, 1], heads, kv, dim, behind=1)
     check_attention(plan, cache, q, [1, 0], max_new=2)
+
+
+@pytest.mark.parametrize("rows,heads,dim,rot", [(3700, 3, 128, 48), (3601, 40, 64, 64), (4001, 1, 64, 64), (3650, 1, 128, 16),
+                                                (3999, 33, 128, 128), (700, 2, 64, 32)])
+def test_rope_many_rows(rows, heads, dim, rot):
+    # blocks of every number of rows, the last one not full, some rows left alone
+    rng = np.random.default_rng(rows)
+    x = bf16(rng, rows, heads, dim)
+    pos = rng.integers(0, 100000, rows)
+    pos[::7] = -1
+    f, mag = oc.frequencies(rot)
+    want, kept = oc.rope(f64(x), np.maximum(pos, 0), f, mag, False), x.clone()
+    out = torch.full_like(x, 3.0)
+    dg.rope(x, ints(pos.tolist()), dg.RopeFrequencies(rot), out=out)
+    # a bf16 rounding, and 2^-21 of a pair's length as in the append
+    size = np.abs(f64(x)).max(-1, keepdims=True)
+    tol = 2.0 ** -8 * np.abs(want) + 2.0 ** -21 * math.sqrt(2) * size
+    there = pos >= 0
+    assert np.all(np.abs(f64(out) - want)[there] <= tol[there]) and (out[torch.from_numpy(~there).cuda()] == 3).all()
+    assert torch.equal(x, kept)
+    dg.rope(x, ints(pos.tolist()), dg.RopeFrequencies(rot), out=x)  # in place
+    assert torch.equal(x[torch.from_numpy(there).cuda()], out[torch.from_numpy(there).cuda()])
+    assert torch.equal(x[torch.from_numpy(~there).cuda()], kept[torch.from_numpy(~there).cuda()])
