@@ -533,7 +533,10 @@ def generate_blocks_context(plan: ContextPlan, E, hidden_fn, n_blocks: int, h_bu
     ``plan`` holds the tables of the block's provisional rows whenever
     ``hidden_fn`` is called, for ``context_append`` and
     ``context_attention``; the batch it held before the call is committed
-    first."""
+    first.  After block j's last step ``hidden_fn(j, params.max_steps, canvas,
+    committed, h_buf)`` is called once more, with the finished canvas, to encode
+    it: what it appends then is what the next plan commits (``h_buf`` is not
+    read)."""
     return _run_blocks(plan, E, hidden_fn, n_blocks, h_buf, blocks, canvas, prev_argmax, accept, entropy, sampled,
                        argmax, stop, ws, params, e_scale, stream)
 

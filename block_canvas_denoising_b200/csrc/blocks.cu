@@ -3,13 +3,15 @@
 // denoised from noise until it settles, then encoded and appended to the
 // context the next block is conditioned on).
 //
-// The model (encoder, KV cache, denoiser) is the caller's: it is reached
-// through the hidden-state callback, which receives the blocks committed so
-// far.  This file adds the noise canvas a block starts from (uniform over
-// the vocabulary, Figure 3) and the driver that chains the adaptive loop over
+// The model (encoder, denoiser) is the caller's: it is reached through the
+// hidden-state callback, which receives the blocks committed so far.  This
+// file adds the noise canvas a block starts from (uniform over the
+// vocabulary, Figure 3) and the driver that chains the adaptive loop over
 // blocks, each block drawing its own random streams (the block index enters
-// the Philox counter's step word).  With a context (context.cu) the driver
-// also plans every block's slots in it before the block's first step.
+// the Philox counter's step word).  With a context (context.cu: the tables and
+// the cache of keys and values) the driver also plans every block's slots in
+// it before the block's first step, and has the callback encode the finished
+// block into them before the next plan commits it.
 #include <string.h>
 
 #include "context.h"
@@ -121,6 +123,11 @@ dg_status run_blocks(const dg_shape* shape, const dg_params* params, const void*
     if (cudaMemcpyAsync(blocks + static_cast<size_t>(j) * rows, canvas, sizeof(int32_t) * rows,
                         cudaMemcpyDeviceToDevice, cs) != cudaSuccess)
       return DG_ERR_CUDA;
+    // encode: the slots hold what the last step's callback appended for the
+    // canvas that step started from; the finished canvas goes over it while
+    // the batch is still provisional
+    if (ctx != nullptr && block_trampoline(params->max_steps, canvas, h_buf, &call, stream) != 0)
+      return DG_ERR_CALLBACK;
   }
   if (cudaStreamSynchronize(cs) != cudaSuccess) return DG_ERR_CUDA;
   return DG_OK;

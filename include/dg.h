@@ -535,9 +535,14 @@ dg_status dg_context_attention(const dg_context* ctx, const dg_context_cache* ca
  * block's B * 256 provisional rows (dg_context_plan with 256 added tokens per
  * request, the batch before committed), so that hidden_fn finds the tables
  * of its canvas in `ctx` and appends to and attends over its own layers'
- * caches.  ctx->B = shape->B and ctx->rows >= B * 256; `add` is an int32 [B]
+ * caches.  After the block's last step hidden_fn is called once more, with
+ * k = params->max_steps (no step has that number) and the finished canvas, to
+ * encode it: the keys and values it appends then, causally ([Press]), are those
+ * that the next plan commits.  It need not write h_out in that call.
+ * ctx->B = shape->B and ctx->rows >= B * 256; `add` is an int32 [B]
  * device buffer that the call fills.  A batch planned before the call (the
- * prompts) is committed by block 0's plan; the last block stays provisional.
+ * prompts) is committed by block 0's plan; the last block, encoded too, stays
+ * provisional.
  * DG_ERR_CAPACITY when a block does not fit. */
 dg_status dg_generate_blocks_context(const dg_shape* shape, const dg_params* params, const void* E,
                                      const float* e_scale, int32_t n_blocks, dg_block_hidden_fn hidden_fn,
