@@ -9,6 +9,7 @@ raise ``DGError``.
 from __future__ import annotations
 
 import ctypes
+import itertools
 import os
 from dataclasses import dataclass
 
@@ -58,7 +59,7 @@ class _Context(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int32), ("rows", ctypes.c_int32), ("pages", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in (
                     "table", "held", "free_list", "free_count", "lens", "start", "positions", "slots", "runs",
-                    "free_next", "status")]
+                    "free_next", "status", "epoch")]
 
 
 class _Heads(ctypes.Structure):
@@ -73,7 +74,7 @@ class _RopeArgs(ctypes.Structure):
 class _Cache(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_int32), ("heads", ctypes.c_int32), ("dim", ctypes.c_int32),
                 ("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p)]
+                ("v_scale", ctypes.c_void_p), ("kept", ctypes.c_void_p)]
 
 
 SELECT_CUMSUM = 0
@@ -179,6 +180,8 @@ def lib() -> ctypes.CDLL:
         L.dg_rope_frequencies.restype = ctypes.c_int
         L.dg_rope.argtypes = [P, P, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, P, P, P]
         L.dg_rope.restype = ctypes.c_int
+        L.dg_context_kept_size.argtypes = [ctypes.c_int32] * 3
+        L.dg_context_kept_size.restype = ctypes.c_size_t
         L.dg_context_append.argtypes = [P, P, P, P, P, P]
         L.dg_context_append.restype = ctypes.c_int
         L.dg_context_workspace_size.argtypes = [ctypes.c_int32] * 4
@@ -586,6 +589,8 @@ def _run_blocks(plan, E, hidden_fn, n_blocks, h_buf, blocks, canvas, prev_argmax
 
 PAGE = 64  # token slots per page
 
+_plans = itertools.count()
+
 _ROPE_SCALING = {"none": 0, "linear": 1, "ntk": 2, "parts": 3}
 
 
@@ -637,7 +642,7 @@ class ContextPlan:
     ``table`` [B, max_pages], ``held`` [B], ``free_list`` [pages],
     ``free_count`` [1]; results ``lens`` [B], ``start`` [B + 1], ``positions``
     and ``slots`` [rows], ``runs`` [rows // 64 + 2 B, 4], ``free_next`` [1],
-    ``status`` [2].  A new plan is empty, all pages free."""
+    ``status`` [2], ``epoch`` [1].  A new plan is empty, all pages free."""
 
     def __init__(self, B: int, rows: int, pages: int, max_pages: int, device=None):
         import torch
@@ -657,10 +662,11 @@ class ContextPlan:
         self.runs = zeros(rows // PAGE + 2 * B, 4)
         self.runs[:, 0] = -1
         self.status = zeros(2)
+        self.epoch = zeros(1) + next(_plans) * 0x9E3779B1 % 2 ** 31  # plans that share a cache start far apart
         self.add = zeros(B)  # lengths of generate_blocks_context
         self._c = _Context(B, rows, pages, max_pages, *(getattr(self, n).data_ptr() for n in (
             "table", "held", "free_list", "free_count", "lens", "start", "positions", "slots", "runs", "free_next",
-            "status")))
+            "status", "epoch")))
         self._ref = ctypes.byref(self._c)
 
 
@@ -729,7 +735,9 @@ def rope(x, positions, frequencies: RopeFrequencies, out=None, stream=None):
 class ContextCache:
     """One layer's cache (``dg_context_cache``): E4M3 codes ``k``, ``v`` (uint8
     [pages, heads, 64, dim]) and power-of-two scales ``k_scale``, ``v_scale``
-    (float32 [pages, heads])."""
+    (float32 [pages, heads]); ``kept``: held tokens' codes as they were before a
+    provisional batch, which ``context_append`` keeps for itself (one page a
+    request, 256 at most)."""
 
     def __init__(self, pages: int, heads: int, dim: int, device=None):
         import torch
@@ -740,16 +748,19 @@ class ContextCache:
         self.v = torch.zeros_like(self.k)
         self.k_scale = torch.ones((pages, heads), dtype=torch.float32, device=device)
         self.v_scale = torch.ones_like(self.k_scale)
+        self.kept = torch.zeros(lib().dg_context_kept_size(pages, heads, dim), dtype=torch.uint8, device=device)
         self.device = self.k.device
         self._c = _Cache(self.pages, self.heads, self.dim, self.k.data_ptr(), self.v.data_ptr(),
-                         self.k_scale.data_ptr(), self.v_scale.data_ptr())
+                         self.k_scale.data_ptr(), self.v_scale.data_ptr(), self.kept.data_ptr())
         self._ref = ctypes.byref(self._c)
 
 
 def context_append(plan: ContextPlan, cache: ContextCache, k, v, rope: RopeFrequencies = None, stream=None) -> None:
     """Write the batch's keys (rotated by their positions with ``rope``) and
     values, bfloat16 [plan.rows, heads, dim], into their slots of ``cache``
-    (``dg_context_append``)."""
+    (``dg_context_append``).  Rows that take the place of a batch's (a canvas's
+    next step) are best planned again first: the append then starts from the
+    held tokens as they were committed."""
     dev = plan.device
     _need(cache.device == dev and (rope is None or rope.freq.device == dev),
           "the cache and the frequencies must be on the plan's device")

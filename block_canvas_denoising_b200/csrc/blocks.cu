@@ -42,16 +42,22 @@ namespace {
 
 // Adapts the block callback to the loop's: the loop calls back with
 // (k, canvas, h_out); the block, the committed prefix and the caller's
-// context ride along here.
+// context ride along here.  With a context every call but a block's first,
+// whose plan commits the block before, is preceded by the same plan again: the
+// call's appends then start from the held tokens as they were committed.
 struct BlockCall {
   dg_block_hidden_fn fn;
   void* user;
   int32_t block;
   const int32_t* committed;
+  const dg_context* ctx;
+  const int32_t* add;
+  dg_status status;  // of a plan that failed
 };
 
 int block_trampoline(int32_t k, const int32_t* canvas, void* h_out, void* user, void* stream) {
-  const BlockCall* c = static_cast<const BlockCall*>(user);
+  BlockCall* c = static_cast<BlockCall*>(user);
+  if (c->ctx != nullptr && k > 0 && (c->status = dg_context_plan(c->ctx, c->add, nullptr, 0, stream)) != DG_OK) return 1;
   return c->fn(c->block, k, canvas, c->committed, h_out, c->user, stream);
 }
 
@@ -114,10 +120,11 @@ dg_status run_blocks(const dg_shape* shape, const dg_params* params, const void*
       if ((st = dg_context_status(ctx, stream)) != DG_OK) return st;
     }
     memset(has_prev, 0, sizeof(has_prev));
-    BlockCall call{hidden_fn, user, j, j > 0 ? blocks : nullptr};
+    BlockCall call{hidden_fn, user, j, j > 0 ? blocks : nullptr, ctx, add, DG_OK};
     st = dg_denoise_loop(shape, &pj, E, e_scale, block_trampoline, &call, 0, h_buf, canvas, prev_argmax,
                          has_prev, steps_taken + static_cast<size_t>(j) * B, accept, entropy, sampled, argmax,
                          stop, workspace, ws_bytes, stream);
+    if (call.status != DG_OK) return call.status;
     if (st != DG_OK) return st;
     // append: the committed block joins the context of the next ones
     if (cudaMemcpyAsync(blocks + static_cast<size_t>(j) * rows, canvas, sizeof(int32_t) * rows,
@@ -127,7 +134,7 @@ dg_status run_blocks(const dg_shape* shape, const dg_params* params, const void*
     // canvas that step started from; the finished canvas goes over it while
     // the batch is still provisional
     if (ctx != nullptr && block_trampoline(params->max_steps, canvas, h_buf, &call, stream) != 0)
-      return DG_ERR_CALLBACK;
+      return call.status != DG_OK ? call.status : DG_ERR_CALLBACK;
   }
   if (cudaStreamSynchronize(cs) != cudaSuccess) return DG_ERR_CUDA;
   return DG_OK;

@@ -200,6 +200,7 @@ context_plan_kernel(const dg_context c, const int32_t* __restrict__ add, const u
       c.free_count[0] = kept;
       c.free_next[0] = kept - (ok ? static_cast<int>(tot.v[1]) : 0);
       c.status[0] = code;
+      if (c.epoch != nullptr) c.epoch[0] = static_cast<int32_t>(static_cast<uint32_t>(c.epoch[0]) + 1u);
     }
   }
 }
@@ -419,6 +420,109 @@ DG_DEV uint2 e4m3_chunk(const float (&x)[8], float inv) {
                     e4m3_pair(x[4] * inv, x[5] * inv) | e4m3_pair(x[6] * inv, x[7] * inv) << 16);
 }
 
+// ---- held tokens on a page that a provisional batch goes on filling
+// A batch may be planned over, and then the held codes it had rounded again
+// must be there as they were.  They are few -- one page a request at most -- so
+// they are put aside when the scale grows, in a place of the page's own
+// (`pages` up to DG_MAX_B) or of its request's, with a tag that says of which
+// page, which tokens and which plan they are, and what the append left in the
+// page.  The next plan's append begins with them if the page is still that.
+struct KeptTag {
+  int32_t page, off;    // held tokens [0, off) of this page; off = 0: nothing
+  uint32_t epoch;       // the plan whose batch made the scale grow
+  float base, grown;    // scales before and after
+  uint32_t check[2];    // sums over the codes as rounded again
+  uint32_t unused;
+};
+static_assert(sizeof(KeptTag) == 32, "two 16-byte words");
+constexpr size_t kKeptAlign = 256;
+inline __host__ __device__ int kept_slots(int pages) { return pages < DG_MAX_B ? pages : DG_MAX_B; }
+inline __host__ __device__ size_t kept_tag_bytes(int pages, int heads) {
+  return (static_cast<size_t>(kept_slots(pages)) * 2 * heads * sizeof(KeptTag) + kKeptAlign - 1) / kKeptAlign * kKeptAlign;
+}
+
+// Two sums over a thread's words, over the block; ends with every thread past
+// its reads of `sums` but the last ones.
+DG_DEV uint2 block_check(uint32_t a, uint32_t b, uint32_t* sums /* [2][threads / 32] shared */) {
+  const int warps = blockDim.x >> 5;
+  a = __reduce_add_sync(0xffffffffu, a);
+  b = __reduce_add_sync(0xffffffffu, b);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) {
+    sums[threadIdx.x >> 5] = a;
+    sums[warps + (threadIdx.x >> 5)] = b;
+  }
+  __syncthreads();
+  uint2 t = make_uint2(0, 0);
+  for (int w = 0; w < warps; ++w) {
+    t.x += sums[w];
+    t.y += sums[warps + w];
+  }
+  return t;
+}
+DG_DEV void check_word(uint32_t i, uint32_t w, uint32_t& a, uint32_t& b) {
+  uint32_t x = (w + i * 0x9E3779B9u) * 0x85EBCA6Bu;
+  x ^= x >> 15;
+  a += x * 0xC2B2AE35u;
+  b += (x ^ (x >> 13)) * 0x27D4EB2Fu;
+}
+
+// The scale of a page that keeps `words` words of codes under scale `old` when
+// the new rows want `s`, and the kept codes under it.  All threads of the
+// block; tag null: nothing is put aside.  Out of line: it runs where a scale
+// grows or has grown, and its registers would cost the others.
+__device__ __noinline__ float settle_kept(uint32_t* codes, int words, float old, float s, int page, int off,
+                                          uint32_t epoch, KeptTag* tag, uint32_t* kept, uint32_t* sums) {
+  bool mine = false, restore = false;  // the tag is of this page as it stands: of this plan's batch, or of another's
+  float base = old;
+  if (tag != nullptr && tag->page == page && tag->off == off && __float_as_uint(tag->grown) == __float_as_uint(old)) {
+    uint32_t a = 0, b = 0;
+    for (int i = threadIdx.x; i < words; i += blockDim.x) check_word(i, codes[i], a, b);
+    const uint2 sum = block_check(a, b, sums);
+    const bool same = sum.x == tag->check[0] && sum.y == tag->check[1];
+    mine = same && tag->epoch == epoch;
+    restore = same && !mine;
+    if (restore) base = tag->base;
+  }
+  const bool grows = s > base;
+  const float ratio = base / s;
+  uint32_t a = 0, b = 0;
+  for (int i = threadIdx.x; i < words; i += blockDim.x) {
+    uint32_t w = restore ? kept[i] : codes[i];
+    if (grows) {
+      if (tag != nullptr && !mine && !restore) kept[i] = w;
+      float f[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __half_raw hr = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(w >> (8 * j)), __NV_E4M3);
+        f[j] = __half2float(*reinterpret_cast<const __half*>(&hr)) * ratio;
+      }
+      w = e4m3_pair(f[0], f[1]) | e4m3_pair(f[2], f[3]) << 16;
+    }
+    if (grows || restore) codes[i] = w;
+    check_word(i, w, a, b);
+  }
+  if (tag != nullptr && (grows || restore)) {
+    const uint2 sum = block_check(a, b, sums);
+    if (threadIdx.x == 0) {
+      if (grows) {
+        if (!mine) {
+          tag->page = page;
+          tag->off = off;
+          tag->epoch = epoch;
+          tag->base = base;
+        }
+        tag->grown = s;
+        tag->check[0] = sum.x;
+        tag->check[1] = sum.y;
+      } else {
+        tag->off = 0;  // the page is as it was
+      }
+    }
+  }
+  return grows ? s : base;
+}
+
 // One CTA per (run, `per` kv heads, k or v): it owns those pages' scales and
 // all of their codes, so no two CTAs meet.  A thread has kMine units of 16
 // elements (a run of 64 rows fills the block); they stay in registers between
@@ -442,8 +546,25 @@ context_append_kernel(const dg_context c, const dg_context_cache cache, const dg
   constexpr int kRows = kThreads / kUnits;        // rows between a thread's units
   __shared__ float s_top[3][kWarps];
   __shared__ __align__(16) float2 s_turn[DG_PAGE][kDim / 2];
+  __shared__ uint32_t s_grown[1024 / 32];  // heads whose kept codes an earlier plan's batch had rounded again
+  __shared__ uint32_t s_check[2 * kWarps];
+  __shared__ int s_owner[kWarps];
   wait_for_previous_kernel();
   allow_next_kernel();
+  // the requests' first rows, to find the run's: on their way with the run
+  const bool keeps = cache.kept != nullptr && c.epoch != nullptr, by_request = keeps && cache.pages > DG_MAX_B;
+  constexpr int kOwn = DG_MAX_B / kThreads;
+  int start0[kOwn], start1[kOwn];
+#pragma unroll
+  for (int i = 0; i < kOwn; ++i) {
+    const int r = threadIdx.x + i * kThreads;
+    start0[i] = start1[i] = -1;
+    if (by_request && r < c.B) {
+      start0[i] = c.start[r];
+      start1[i] = c.start[r + 1];
+    }
+  }
+  const uint32_t epoch = keeps ? static_cast<uint32_t>(*c.epoch) : 0u;
   const int4 run = reinterpret_cast<const int4*>(c.runs)[blockIdx.x];
   const int page = run.x, row0 = run.y, off = run.z, n = run.w;
   if (page < 0 || page >= cache.pages || n <= 0 || off < 0 || off + n > DG_PAGE || row0 < 0 || row0 + n > c.rows) return;
@@ -472,6 +593,32 @@ context_append_kernel(const dg_context c, const dg_context_cache cache, const dg
     }
   };
   load(src);
+  KeptTag* tags = nullptr;  // of this block's heads, where codes are kept aside
+  uint32_t* kept = nullptr;
+  if (keeps && off > 0) {
+    int slot = page;
+    if (by_request) {
+      int r = -1;
+#pragma unroll
+      for (int i = 0; i < kOwn; ++i) {
+        if (start0[i] == row0 && start1[i] > row0) r = threadIdx.x + i * kThreads;
+      }
+      r = __reduce_max_sync(0xffffffffu, r);
+      if ((threadIdx.x & 31) == 0) s_owner[threadIdx.x >> 5] = r;
+    }
+    if (threadIdx.x < 32) s_grown[threadIdx.x] = 0;
+    __syncthreads();
+    if (by_request) slot = __reduce_max_sync(0xffffffffu, s_owner[threadIdx.x & (kWarps - 1)]);
+    if (slot >= 0) {
+      const size_t at = (static_cast<size_t>(slot) * 2 + (is_k ? 0 : 1)) * cache.heads + head0;
+      tags = reinterpret_cast<KeptTag*>(cache.kept) + at;
+      kept = reinterpret_cast<uint32_t*>(cache.kept + kept_tag_bytes(cache.pages, cache.heads) + at * DG_PAGE * kDim);
+      for (int h = threadIdx.x; h < heads; h += kThreads) {  // read after the next barrier
+        const int4 t = *reinterpret_cast<const int4*>(tags + h);
+        if (t.x == page && t.y == off && static_cast<uint32_t>(t.z) != epoch) atomicOr(&s_grown[h >> 5], 1u << (h & 31));
+      }
+    }
+  }
   if (rot16 > 0) {
     const int half = 8 * rot16, stride = kThreads / half;
     const int j = threadIdx.x % half;  // this thread's frequency; the block's threads walk the rows
@@ -541,22 +688,13 @@ context_append_kernel(const dg_context c, const dg_context_cache cache, const dg
     const int e = scale_exponent(top);
     float s = power_of_two(e), inv = power_of_two(-e);  // |e| <= 120
     if (off > 0) {
-      if (!(s > old)) {
+      const bool grown = tags != nullptr && (s_grown[h >> 5] >> (h & 31) & 1u);
+      if (s > old || grown)
+        s = settle_kept(reinterpret_cast<uint32_t*>(codes), off * kDim / 4, old, s, page, off, epoch,
+                        tags != nullptr ? tags + h : nullptr, kept + static_cast<size_t>(h) * (DG_PAGE * kDim / 4), s_check);
+      else
         s = old;
-        inv = 1.0f / old;  // exact: a power of two
-      } else {  // kept tokens move to the larger scale
-        const float ratio = old / s;
-        for (int i = threadIdx.x; i < off * kDim / 4; i += kThreads) {
-          const uint32_t w = reinterpret_cast<const uint32_t*>(codes)[i];
-          float f[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __half_raw hr = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(w >> (8 * j)), __NV_E4M3);
-            f[j] = __half2float(*reinterpret_cast<const __half*>(&hr)) * ratio;
-          }
-          reinterpret_cast<uint32_t*>(codes)[i] = e4m3_pair(f[0], f[1]) | e4m3_pair(f[2], f[3]) << 16;
-        }
-      }
+      inv = 1.0f / s;  // exact: a power of two
     }
     uint8_t* dst = codes + (off + row) * kDim;
 #pragma unroll
@@ -586,7 +724,8 @@ dg_status check_context(const dg_context* c) {
     return DG_ERR_UNSUPPORTED_SHAPE;
   if (!aligned(c->table, 4) || !aligned(c->held, 4) || !aligned(c->free_list, 4) || !aligned(c->free_count, 4) ||
       !aligned(c->lens, 4) || !aligned(c->start, 4) || !aligned(c->positions, 4) || !aligned(c->slots, 8) ||
-      !aligned(c->runs, 16) || !aligned(c->free_next, 4) || !aligned(c->status, 4))
+      !aligned(c->runs, 16) || !aligned(c->free_next, 4) || !aligned(c->status, 4) ||
+      (c->epoch != nullptr && !aligned(c->epoch, 4)))
     return DG_ERR_INVALID_ARG;
   return DG_OK;
 }
@@ -605,7 +744,8 @@ dg_status check_cache(const dg_context_cache* c, const dg_context* ctx) {
   if ((c->dim != 64 && c->dim != 128) || c->heads < 1 || c->heads > 1024 || c->pages != ctx->pages)
     return DG_ERR_UNSUPPORTED_SHAPE;
   if (static_cast<int64_t>(c->pages) * c->heads * DG_PAGE > 0x7fffffffll - 1025 * DG_PAGE) return DG_ERR_UNSUPPORTED_SHAPE;
-  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4))
+  if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
+      (c->kept != nullptr && !aligned(c->kept, 16)))
     return DG_ERR_INVALID_ARG;
   return DG_OK;
 }
@@ -716,6 +856,11 @@ dg_status dg_rope(const dg_heads* x, const dg_heads* out, int32_t rows, int32_t 
       dim == 128 ? start(rope_kernel<128, 1>, rope_kernel<128, 4>, rope_kernel<128, 8>, rope_kernel<128, 32>)
                  : start(rope_kernel<64, 1>, rope_kernel<64, 4>, rope_kernel<64, 8>, rope_kernel<64, 32>);
   return cuda_ok(e, "rope launch") ? DG_OK : DG_ERR_CUDA;
+}
+
+size_t dg_context_kept_size(int32_t pages, int32_t heads, int32_t dim) {
+  if (pages < 1 || pages > (1 << 24) || heads < 1 || heads > 1024 || (dim != 64 && dim != 128)) return 0;
+  return kept_tag_bytes(pages, heads) + static_cast<size_t>(kept_slots(pages)) * 2 * heads * DG_PAGE * dim;
 }
 
 dg_status dg_context_append(const dg_context* ctx, const dg_context_cache* cache, const dg_heads* k,

@@ -386,7 +386,10 @@ dg_status dg_generate_blocks(const dg_shape* shape, const dg_params* params,
  * request in the batch's tensors, row start[r] + i being token held[r] + i.
  * A batch is provisional: its tokens occupy slots behind the held ones, and
  * may be written again (every denoising step of a canvas does), until a
- * later plan commits them.  One dg_context serves all layers of a model;
+ * later plan commits them.  Within one plan a page's scale only grows: rows that
+ * take the place of a batch's (a canvas's next step) are best planned again,
+ * not committed, before they are appended (dg_context_append says why).  One
+ * dg_context serves all layers of a model;
  * each layer has a dg_context_cache of its own. */
 #define DG_PAGE 64
 /* Entries of dg_context.runs for a batch of up to `rows` rows. */
@@ -412,6 +415,8 @@ typedef struct {
                           tokens), in row order; (-1, 0, 0, 0) behind the last */
   int32_t* free_next;  /* [1] free pages once the batch is committed */
   int32_t* status;     /* [2] outcome of the last plan; latch of dg_context_append */
+  int32_t* epoch;      /* [1] number of the plan, any value to begin with (contexts that
+                          share a cache: different ones); NULL: see dg_context_cache.kept */
 } dg_context;
 
 /* dg_context_plan -- block tables and slot maps of a batch, from request
@@ -485,7 +490,16 @@ typedef struct {
   uint8_t* v;
   float* k_scale;              /* [pages][heads] */
   float* v_scale;
+  /* Held tokens as they were before a provisional batch had their page's codes
+   * rounded again: dg_context_kept_size() bytes on the device, 16-byte
+   * aligned, zeroed once.  NULL (or a context without epoch): nothing is kept,
+   * for a caller that commits every batch as it was first appended. */
+  uint8_t* kept;
 } dg_context_cache;
+
+/* Bytes of dg_context_cache.kept (0 if invalid): the codes of one page and head
+ * for min(pages, DG_MAX_B) pages, for keys and for values. */
+size_t dg_context_kept_size(int32_t pages, int32_t heads, int32_t dim);
 
 /* dg_context_append -- keys and values of the batch's rows into their slots.
  *   k, v   bf16 [ctx->rows][heads][dim]; rows from start[B] on are not read.
@@ -493,7 +507,13 @@ typedef struct {
  * Each (page, head) of a run gets the least power of two s with
  * max |x| <= 448 s over the run (at least 2^-100; 1 when all are 0), but not
  * less than its old scale while it keeps tokens before the run; when it
- * grows, the kept codes are rounded again.  Keys are rotated in float32 and
+ * grows, the kept codes are rounded again.  Where the tokens before the run are
+ * held ones, that lasts only as long as the plan: the first append of a later
+ * plan that opens the run at the same place starts from the codes and the
+ * scale from before (cache->kept), so that a batch which was planned over
+ * leaves nothing in the held tokens.  (It does so if the page is as the
+ * earlier append left it; held tokens written otherwise stand as they are.)
+ * Keys are rotated in float32 and
  * rounded once, to nearest even.  A NaN is stored as 0 and an infinity as
  * +-448 s with DG_ERR_VALUE latched (dg_context_status); neither counts
  * towards s.  Slots behind the batch are left as they were. */
@@ -535,7 +555,8 @@ dg_status dg_context_attention(const dg_context* ctx, const dg_context_cache* ca
  * block's B * 256 provisional rows (dg_context_plan with 256 added tokens per
  * request, the batch before committed), so that hidden_fn finds the tables
  * of its canvas in `ctx` and appends to and attends over its own layers'
- * caches.  After the block's last step hidden_fn is called once more, with
+ * caches.  Every call finds the block planned anew, so a step leaves nothing in
+ * the held tokens.  After the block's last step hidden_fn is called once more, with
  * k = params->max_steps (no step has that number) and the finished canvas, to
  * encode it: the keys and values it appends then, causally ([Press]), are those
  * that the next plan commits.  It need not write h_out in that call.

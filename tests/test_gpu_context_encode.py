@@ -68,7 +68,7 @@ def held_values(plan, layer, lens):
     return got
 
 
-@pytest.mark.parametrize("prompts", [[128, 64]])
+@pytest.mark.parametrize("prompts", [[128, 64], [100, 7]])
 def test_a_block_is_encoded_before_it_is_committed(prompts):
     E_bits = synth.embedder_normal(V, D, seed=1)
     E = to_dev_bf16(E_bits)
