@@ -98,6 +98,7 @@ context_plan_kernel(const dg_context c, const int32_t* __restrict__ add, const u
   allow_next_kernel();
 
   const int64_t free0 = *(commit ? c.free_next : c.free_count);
+  const uint32_t epoch = c.epoch != nullptr ? static_cast<uint32_t>(*c.epoch) : 0u;
   int64_t held = 0, a = 0, gone = 0, need = 0, touched = 0;
   if (tid < B) {
     held = commit ? c.lens[tid] : c.held[tid];
@@ -200,7 +201,7 @@ context_plan_kernel(const dg_context c, const int32_t* __restrict__ add, const u
       c.free_count[0] = kept;
       c.free_next[0] = kept - (ok ? static_cast<int>(tot.v[1]) : 0);
       c.status[0] = code;
-      if (c.epoch != nullptr) c.epoch[0] = static_cast<int32_t>(static_cast<uint32_t>(c.epoch[0]) + 1u);
+      if (c.epoch != nullptr) c.epoch[0] = static_cast<int32_t>(epoch + 1u);
     }
   }
 }
@@ -426,7 +427,10 @@ DG_DEV uint2 e4m3_chunk(const float (&x)[8], float inv) {
 // they are put aside when the scale grows, in a place of the page's own
 // (`pages` up to DG_MAX_B) or of its request's, with a tag that says of which
 // page, which tokens and which plan they are, and what the append left in the
-// page.  The next plan's append begins with them if the page is still that.
+// page.  The next plan's append begins with them if the page is still that.  A
+// byte for each page says how many tokens it held when that last happened: all
+// that an append reads where nothing has grown.  (With every head's tag read in
+// any case, 32 requests x 8 heads x 1 row took 3.8 us instead of 3.4.)
 struct KeptTag {
   int32_t page, off;    // held tokens [0, off) of this page; off = 0: nothing
   uint32_t epoch;       // the plan whose batch made the scale grow
@@ -435,14 +439,22 @@ struct KeptTag {
   uint32_t unused;
 };
 static_assert(sizeof(KeptTag) == 32, "two 16-byte words");
-constexpr size_t kKeptAlign = 256;
-inline __host__ __device__ int kept_slots(int pages) { return pages < DG_MAX_B ? pages : DG_MAX_B; }
-inline __host__ __device__ size_t kept_tag_bytes(int pages, int heads) {
-  return (static_cast<size_t>(kept_slots(pages)) * 2 * heads * sizeof(KeptTag) + kKeptAlign - 1) / kKeptAlign * kKeptAlign;
+// dg_context_cache.kept: bytes [pages], tags and codes [slots][k, v][heads].
+struct KeptLayout {
+  int slots;
+  size_t tags, codes, total;
+};
+inline __host__ __device__ KeptLayout kept_layout(int pages, int heads, int dim) {
+  KeptLayout l;
+  l.slots = pages < DG_MAX_B ? pages : DG_MAX_B;
+  const size_t places = static_cast<size_t>(l.slots) * 2 * heads;
+  l.tags = (static_cast<size_t>(pages) + 255) / 256 * 256;
+  l.codes = l.tags + (places * sizeof(KeptTag) + 255) / 256 * 256;
+  l.total = l.codes + places * DG_PAGE * dim;
+  return l;
 }
 
-// Two sums over a thread's words, over the block; ends with every thread past
-// its reads of `sums` but the last ones.
+// Two sums over the block's threads.
 DG_DEV uint2 block_check(uint32_t a, uint32_t b, uint32_t* sums /* [2][threads / 32] shared */) {
   const int warps = blockDim.x >> 5;
   a = __reduce_add_sync(0xffffffffu, a);
@@ -467,15 +479,39 @@ DG_DEV void check_word(uint32_t i, uint32_t w, uint32_t& a, uint32_t& b) {
   b += (x ^ (x >> 13)) * 0x27D4EB2Fu;
 }
 
-// The scale of a page that keeps `words` words of codes under scale `old` when
-// the new rows want `s`, and the kept codes under it.  All threads of the
-// block; tag null: nothing is put aside.  Out of line: it runs where a scale
-// grows or has grown, and its registers would cost the others.
-__device__ __noinline__ float settle_kept(uint32_t* codes, int words, float old, float s, int page, int off,
-                                          uint32_t epoch, KeptTag* tag, uint32_t* kept, uint32_t* sums) {
+// The scale of head h of run (page, row0, off, .) whose page keeps tokens under
+// scale `old` when the new rows want `s`, and the kept codes under it.  All
+// threads of the block.
+template <int kDim>
+DG_DEV float settle_kept(const dg_context& c, const dg_context_cache& cache, bool is_k, int h, int page,
+                                          int row0, int off, float old, float s, uint32_t* sums) {
+  const size_t at_page = static_cast<size_t>(page) * cache.heads + h;
+  uint32_t* codes = reinterpret_cast<uint32_t*>((is_k ? cache.k : cache.v) + at_page * DG_PAGE * kDim);
+  const int words = off * kDim / 4;
+  KeptTag* tag = nullptr;  // null: nothing is put aside
+  uint32_t* kept = nullptr;
+  uint32_t epoch = 0;
+  if (cache.kept != nullptr && c.epoch != nullptr) {
+    int slot = page;
+    if (cache.pages > DG_MAX_B) {  // the request whose first row this is, plus 1
+      uint32_t r = 0;
+      for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
+        if (c.start[i] == row0 && c.start[i + 1] > row0) r = i + 1;
+      }
+      slot = static_cast<int>(block_check(r, 0, sums).x) - 1;
+    }
+    if (slot >= 0 && slot < DG_MAX_B) {
+      const KeptLayout l = kept_layout(cache.pages, cache.heads, kDim);
+      const size_t at = (static_cast<size_t>(slot) * 2 + (is_k ? 0 : 1)) * cache.heads + h;
+      tag = reinterpret_cast<KeptTag*>(cache.kept + l.tags) + at;
+      kept = reinterpret_cast<uint32_t*>(cache.kept + l.codes + at * DG_PAGE * kDim);
+      epoch = static_cast<uint32_t>(*c.epoch);
+    }
+  }
   bool mine = false, restore = false;  // the tag is of this page as it stands: of this plan's batch, or of another's
   float base = old;
-  if (tag != nullptr && tag->page == page && tag->off == off && __float_as_uint(tag->grown) == __float_as_uint(old)) {
+  if (tag != nullptr && tag->page == page && tag->off == off && __float_as_uint(tag->grown) == __float_as_uint(old) &&
+      (s > old || tag->epoch != epoch)) {
     uint32_t a = 0, b = 0;
     for (int i = threadIdx.x; i < words; i += blockDim.x) check_word(i, codes[i], a, b);
     const uint2 sum = block_check(a, b, sums);
@@ -485,6 +521,7 @@ __device__ __noinline__ float settle_kept(uint32_t* codes, int words, float old,
     if (restore) base = tag->base;
   }
   const bool grows = s > base;
+  if (!grows && !restore) return old;
   const float ratio = base / s;
   uint32_t a = 0, b = 0;
   for (int i = threadIdx.x; i < words; i += blockDim.x) {
@@ -499,10 +536,10 @@ __device__ __noinline__ float settle_kept(uint32_t* codes, int words, float old,
       }
       w = e4m3_pair(f[0], f[1]) | e4m3_pair(f[2], f[3]) << 16;
     }
-    if (grows || restore) codes[i] = w;
+    codes[i] = w;
     check_word(i, w, a, b);
   }
-  if (tag != nullptr && (grows || restore)) {
+  if (tag != nullptr) {
     const uint2 sum = block_check(a, b, sums);
     if (threadIdx.x == 0) {
       if (grows) {
@@ -515,12 +552,61 @@ __device__ __noinline__ float settle_kept(uint32_t* codes, int words, float old,
         tag->grown = s;
         tag->check[0] = sum.x;
         tag->check[1] = sum.y;
+        cache.kept[page] = static_cast<uint8_t>(off);  // by every head that grows: the same
       } else {
         tag->off = 0;  // the page is as it was
       }
     }
   }
   return grows ? s : base;
+}
+
+constexpr int kMine = 2;
+template <int kDim>
+constexpr int kAppendThreads = DG_PAGE * kDim / 16 / kMine;
+
+// The heads that want[h] > 0 names, of a run behind held tokens: the scale that
+// the rows want is above the page's, or the page's has grown before.  All threads
+// of the block.  Out of line and on its own: within the loop over the heads its
+// registers cost every append (256 requests x 8 heads x 1 row 12.9 us instead of 12.0).
+template <int kDim>
+__device__ __noinline__ void append_grown(const dg_context& c, const dg_context_cache& cache, const dg_heads& in,
+                                          const float2 (*turns)[kDim / 2], int rot16, bool il, bool is_k, int4 run,
+                                          int head0, int heads, const float* want, uint32_t* sums) {
+  constexpr int kUnits = kDim / 16, kRows = kAppendThreads<kDim> / kUnits;
+  const int page = run.x, row0 = run.y, off = run.z, n = run.w;
+  const int u = threadIdx.x % kUnits;
+  int ca, cb;
+  unit_chunks(u, rot16, il, ca, cb);
+  for (int h = head0; h < head0 + heads; ++h) {
+    if (!(want[h - head0] > 0.f)) continue;
+    const size_t at = static_cast<size_t>(page) * cache.heads + h;
+    float* scale = (is_k ? cache.k_scale : cache.v_scale) + at;
+    const float old = *scale;
+    __syncthreads();  // everybody has read it
+    const float s = settle_kept<kDim>(c, cache, is_k, h, page, row0, off, old, want[h - head0], sums);
+    const float inv = 1.0f / s;  // exact: a power of two
+    uint8_t* codes = (is_k ? cache.k : cache.v) + (at * DG_PAGE + off) * kDim;
+    for (int row = threadIdx.x / kUnits; row < n; row += kRows) {
+      const uint8_t* src = static_cast<const uint8_t*>(in.data) + 2 * ((row0 + row) * in.row_stride + h * in.head_stride);
+      float a[8], b[8];
+      unpack8(*reinterpret_cast<const uint4*>(src + 16 * ca), a);
+      unpack8(*reinterpret_cast<const uint4*>(src + 16 * cb), b);
+      if (u < rot16) {
+        float2 tr[8];
+        read_turns(turns[row], u, rot16, tr);
+        rotate_unit(a, b, tr, il);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (a[j] != a[j]) a[j] = 0.f;
+        if (b[j] != b[j]) b[j] = 0.f;
+      }
+      *reinterpret_cast<uint2*>(codes + row * kDim + 8 * ca) = e4m3_chunk(a, inv);
+      *reinterpret_cast<uint2*>(codes + row * kDim + 8 * cb) = e4m3_chunk(b, inv);
+    }
+    if (threadIdx.x == 0) *scale = s;
+  }
 }
 
 // One CTA per (run, `per` kv heads, k or v): it owns those pages' scales and
@@ -533,38 +619,21 @@ __device__ __noinline__ float settle_kept(uint32_t* codes, int words, float old,
 // bound by latency at two blocks an SM (116 registers a thread; squeezed to 78
 // and 64 for three and four blocks: 17.6 and 23.5 us); 32 requests x 1 row in
 // 3.6 us.
-constexpr int kMine = 2;
-template <int kDim>
-constexpr int kAppendThreads = DG_PAGE * kDim / 16 / kMine;
-
 template <int kDim>
 __global__ void __launch_bounds__(kAppendThreads<kDim>)
-context_append_kernel(const dg_context c, const dg_context_cache cache, const dg_heads kin, const dg_heads vin,
-                      const dg_rope_args rope, int has_rope, int per) {
+context_append_kernel(const __grid_constant__ dg_context c, const __grid_constant__ dg_context_cache cache,
+                      const __grid_constant__ dg_heads kin, const __grid_constant__ dg_heads vin, const dg_rope_args rope,
+                      int has_rope, int per) {
   constexpr int kUnits = kDim / 16;  // units per row
   constexpr int kThreads = kAppendThreads<kDim>, kWarps = kThreads / 32;
   constexpr int kRows = kThreads / kUnits;        // rows between a thread's units
   __shared__ float s_top[3][kWarps];
   __shared__ __align__(16) float2 s_turn[DG_PAGE][kDim / 2];
-  __shared__ uint32_t s_grown[1024 / 32];  // heads whose kept codes an earlier plan's batch had rounded again
   __shared__ uint32_t s_check[2 * kWarps];
-  __shared__ int s_owner[kWarps];
+  __shared__ float s_want[1024];  // the scales wanted by heads that append_grown is to do
+  __shared__ bool s_grown;
   wait_for_previous_kernel();
   allow_next_kernel();
-  // the requests' first rows, to find the run's: on their way with the run
-  const bool keeps = cache.kept != nullptr && c.epoch != nullptr, by_request = keeps && cache.pages > DG_MAX_B;
-  constexpr int kOwn = DG_MAX_B / kThreads;
-  int start0[kOwn], start1[kOwn];
-#pragma unroll
-  for (int i = 0; i < kOwn; ++i) {
-    const int r = threadIdx.x + i * kThreads;
-    start0[i] = start1[i] = -1;
-    if (by_request && r < c.B) {
-      start0[i] = c.start[r];
-      start1[i] = c.start[r + 1];
-    }
-  }
-  const uint32_t epoch = keeps ? static_cast<uint32_t>(*c.epoch) : 0u;
   const int4 run = reinterpret_cast<const int4*>(c.runs)[blockIdx.x];
   const int page = run.x, row0 = run.y, off = run.z, n = run.w;
   if (page < 0 || page >= cache.pages || n <= 0 || off < 0 || off + n > DG_PAGE || row0 < 0 || row0 + n > c.rows) return;
@@ -593,32 +662,11 @@ context_append_kernel(const dg_context c, const dg_context_cache cache, const dg
     }
   };
   load(src);
-  KeptTag* tags = nullptr;  // of this block's heads, where codes are kept aside
-  uint32_t* kept = nullptr;
-  if (keeps && off > 0) {
-    int slot = page;
-    if (by_request) {
-      int r = -1;
-#pragma unroll
-      for (int i = 0; i < kOwn; ++i) {
-        if (start0[i] == row0 && start1[i] > row0) r = threadIdx.x + i * kThreads;
-      }
-      r = __reduce_max_sync(0xffffffffu, r);
-      if ((threadIdx.x & 31) == 0) s_owner[threadIdx.x >> 5] = r;
-    }
-    if (threadIdx.x < 32) s_grown[threadIdx.x] = 0;
-    __syncthreads();
-    if (by_request) slot = __reduce_max_sync(0xffffffffu, s_owner[threadIdx.x & (kWarps - 1)]);
-    if (slot >= 0) {
-      const size_t at = (static_cast<size_t>(slot) * 2 + (is_k ? 0 : 1)) * cache.heads + head0;
-      tags = reinterpret_cast<KeptTag*>(cache.kept) + at;
-      kept = reinterpret_cast<uint32_t*>(cache.kept + kept_tag_bytes(cache.pages, cache.heads) + at * DG_PAGE * kDim);
-      for (int h = threadIdx.x; h < heads; h += kThreads) {  // read after the next barrier
-        const int4 t = *reinterpret_cast<const int4*>(tags + h);
-        if (t.x == page && t.y == off && static_cast<uint32_t>(t.z) != epoch) atomicOr(&s_grown[h >> 5], 1u << (h & 31));
-      }
-    }
-  }
+  // Did some head's scale grow with this page at this many held tokens?  One
+  // thread asks, for all to see the same: other blocks may be writing it.
+  int grown_at = 0;
+  if (threadIdx.x == 0 && off > 0 && cache.kept != nullptr) grown_at = cache.kept[page];
+  bool later = false;
   if (rot16 > 0) {
     const int half = 8 * rot16, stride = kThreads / half;
     const int j = threadIdx.x % half;  // this thread's frequency; the block's threads walk the rows
@@ -667,6 +715,7 @@ context_append_kernel(const dg_context c, const dg_context_cache cache, const dg
       top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s_top[buffer][threadIdx.x & (kWarps - 1)])));
     };
     if (zero != zero) top = INFINITY;
+    if (threadIdx.x == 0 && h == 0) s_grown = grown_at == off;
     largest(h & 1);
     if (top > FLT_MAX) {  // seldom: what is not finite does not count, NaN becomes 0
       top = 0.f;
@@ -688,13 +737,17 @@ context_append_kernel(const dg_context c, const dg_context_cache cache, const dg
     const int e = scale_exponent(top);
     float s = power_of_two(e), inv = power_of_two(-e);  // |e| <= 120
     if (off > 0) {
-      const bool grown = tags != nullptr && (s_grown[h >> 5] >> (h & 31) & 1u);
-      if (s > old || grown)
-        s = settle_kept(reinterpret_cast<uint32_t*>(codes), off * kDim / 4, old, s, page, off, epoch,
-                        tags != nullptr ? tags + h : nullptr, kept + static_cast<size_t>(h) * (DG_PAGE * kDim / 4), s_check);
-      else
-        s = old;
-      inv = 1.0f / s;  // exact: a power of two
+      if (s > old || s_grown) {
+        if (!later) {
+          for (int i = threadIdx.x; i < heads; i += kThreads) s_want[i] = 0.f;
+          __syncthreads();
+        }
+        later = true;
+        if (threadIdx.x == 0) s_want[h] = s;
+        continue;
+      }
+      s = old;
+      inv = 1.0f / old;  // exact: a power of two
     }
     uint8_t* dst = codes + (off + row) * kDim;
 #pragma unroll
@@ -704,6 +757,10 @@ context_append_kernel(const dg_context c, const dg_context_cache cache, const dg
       *reinterpret_cast<uint2*>(dst + m * kRows * kDim + 8 * cb) = e4m3_chunk(b[m], inv);
     }
     if (threadIdx.x == 0) *scale = s;
+  }
+  if (later) {
+    __syncthreads();
+    append_grown<kDim>(c, cache, in, s_turn, rot16, il, is_k, run, head0, heads, s_want, s_check);
   }
 }
 
@@ -860,7 +917,7 @@ dg_status dg_rope(const dg_heads* x, const dg_heads* out, int32_t rows, int32_t 
 
 size_t dg_context_kept_size(int32_t pages, int32_t heads, int32_t dim) {
   if (pages < 1 || pages > (1 << 24) || heads < 1 || heads > 1024 || (dim != 64 && dim != 128)) return 0;
-  return kept_tag_bytes(pages, heads) + static_cast<size_t>(kept_slots(pages)) * 2 * heads * DG_PAGE * dim;
+  return kept_layout(pages, heads, dim).total;
 }
 
 dg_status dg_context_append(const dg_context* ctx, const dg_context_cache* cache, const dg_heads* k,

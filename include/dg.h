@@ -497,8 +497,8 @@ typedef struct {
   uint8_t* kept;
 } dg_context_cache;
 
-/* Bytes of dg_context_cache.kept (0 if invalid): the codes of one page and head
- * for min(pages, DG_MAX_B) pages, for keys and for values. */
+/* Bytes of dg_context_cache.kept (0 if invalid): room for the codes of
+ * min(pages, DG_MAX_B) pages, and a byte for every page. */
 size_t dg_context_kept_size(int32_t pages, int32_t heads, int32_t dim);
 
 /* dg_context_append -- keys and values of the batch's rows into their slots.
