@@ -294,7 +294,7 @@ DG_DEV uint64_t add2(uint64_t a, uint64_t b) {
 // degree 4 with the least largest relative error on [-1/2, 1/2] (2.6e-6, found
 // by Remez exchange), n into the exponent.
 // Anything below, -inf too, gives about 2^-126: nothing in float16, and next to
-// nothing in a sum.
+// nothing in a sum.  So does NaN.
 DG_DEV void exp2_poly2(uint64_t v, float& x, float& y) {
   float a, b;
   unpack2(v, a, b);
@@ -329,8 +329,8 @@ DG_DEV float max_of_32(const uint32_t (&u)[32]) {
   return fmaxf(max3(m[0], m[1], m[2]), m[3]);
 }
 
-// A row that saw no key: its maximum never moved.  (A row of NaN has not
-// moved it either, but its sum is NaN.)
+// A row that saw no key: its maximum never moved.  (A row of NaN that saw one
+// has not moved it either, but its sum is NaN.)
 DG_DEV bool saw_nothing(float m, float l) { return m == -FLT_MAX && l < 1.f; }
 
 // A row's place in the batch.
@@ -361,7 +361,7 @@ DG_DEV Row row_of(const AttnParams& p, const Piece& w, int row) {
 // place of the two terms -- a row of bf16 is as long as both -- and every
 // thread then turns its own row: 16 reads in flight a lane and no shuffles.
 // Returns the factor that turns a dot product of the thread's row into a
-// logit in units of log2.
+// logit in units of log2; NaN for a row that is not finite.
 template <int kDim>
 DG_DEV float prepare_q(const AttnParams& p, const Piece& w, uint32_t rho0, uint8_t* q1, uint8_t* q2, int row0) {
   constexpr int kLanes = kDim / 8;           // lanes per row
@@ -442,7 +442,7 @@ DG_DEV float prepare_q(const AttnParams& p, const Piece& w, uint32_t rho0, uint8
   for (int i = 0; i < kH / 2; ++i) terms(i, chunk(2 * i), chunk(2 * i + 1));
 #pragma unroll
   for (int i = kH / 2; i < kH; ++i) terms(i, kept[2 * i - kH], kept[2 * i + 1 - kH]);
-  return finite ? p.scale_log2 * pow2i(-e) : 1.f;
+  return finite ? p.scale_log2 * pow2i(-e) : __int_as_float(0x7fc00000);
 }
 
 template <int kDim>
@@ -872,6 +872,12 @@ attention_tiles_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
           float x, y;
           unpack2(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])), x, y);
           l += (x + y) * pow2i(-static_cast<int>(sc.y));
+          // A row that is not finite: NaN as soon as it sees a key.  Its weights
+          // do not say so, since those by polynomial are numbers.
+          if (fac != fac) {
+            const int key0 = (tile0 + j) * kTilesN;
+            if (sc.x > 0.f && max(key_first, key0) <= min(key_last, key0 + kTilesN - 1)) l = fac;
+          }
           ++T;
           if (j + 1 < tiles) {  // there long since
             wait(sh.sc_full[T % kScaleSlots], (T / kScaleSlots) & 1);
