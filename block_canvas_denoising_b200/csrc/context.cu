@@ -428,9 +428,10 @@ DG_DEV uint2 e4m3_chunk(const float (&x)[8], float inv) {
 // (`pages` up to DG_MAX_B) or of its request's, with a tag that says of which
 // page, which tokens and which plan they are, and what the append left in the
 // page.  The next plan's append begins with them if the page is still that.  A
-// byte for each page says how many tokens it held when that last happened: all
-// that an append reads where nothing has grown.  (With every head's tag read in
-// any case, 32 requests x 8 heads x 1 row took 3.8 us instead of 3.4.)
+// mark beside each scale says in which plan and behind how many tokens it has
+// grown, 0 if it has not: all that an append reads where nothing is to be done.
+// (With every head's tag read in any case, 32 requests x 8 heads x 1 row took
+// 3.8 us instead of 3.5.)
 struct KeptTag {
   int32_t page, off;    // held tokens [0, off) of this page; off = 0: nothing
   uint32_t epoch;       // the plan whose batch made the scale grow
@@ -439,7 +440,8 @@ struct KeptTag {
   uint32_t unused;
 };
 static_assert(sizeof(KeptTag) == 32, "two 16-byte words");
-// dg_context_cache.kept: bytes [pages], tags and codes [slots][k, v][heads].
+DG_DEV uint32_t grown_mark(uint32_t epoch, int off) { return epoch << 6 | static_cast<uint32_t>(off); }  // off < DG_PAGE
+// dg_context_cache.kept: marks [k, v][pages][heads], tags and codes [slots][k, v][heads].
 struct KeptLayout {
   int slots;
   size_t tags, codes, total;
@@ -448,7 +450,7 @@ inline __host__ __device__ KeptLayout kept_layout(int pages, int heads, int dim)
   KeptLayout l;
   l.slots = pages < DG_MAX_B ? pages : DG_MAX_B;
   const size_t places = static_cast<size_t>(l.slots) * 2 * heads;
-  l.tags = (static_cast<size_t>(pages) + 255) / 256 * 256;
+  l.tags = (static_cast<size_t>(pages) * 2 * heads * sizeof(uint32_t) + 255) / 256 * 256;
   l.codes = l.tags + (places * sizeof(KeptTag) + 255) / 256 * 256;
   l.total = l.codes + places * DG_PAGE * dim;
   return l;
@@ -479,133 +481,188 @@ DG_DEV void check_word(uint32_t i, uint32_t w, uint32_t& a, uint32_t& b) {
   b += (x ^ (x >> 13)) * 0x27D4EB2Fu;
 }
 
-// The scale of head h of run (page, row0, off, .) whose page keeps tokens under
-// scale `old` when the new rows want `s`, and the kept codes under it.  All
-// threads of the block.
+constexpr int kMine = 2;
+constexpr int kAppendHeads = 128;  // heads of a block at most
 template <int kDim>
-DG_DEV float settle_kept(const dg_context& c, const dg_context_cache& cache, bool is_k, int h, int page,
-                                          int row0, int off, float old, float s, uint32_t* sums) {
-  const size_t at_page = static_cast<size_t>(page) * cache.heads + h;
-  uint32_t* codes = reinterpret_cast<uint32_t*>((is_k ? cache.k : cache.v) + at_page * DG_PAGE * kDim);
-  const int words = off * kDim / 4;
-  KeptTag* tag = nullptr;  // null: nothing is put aside
-  uint32_t* kept = nullptr;
-  uint32_t epoch = 0;
-  if (cache.kept != nullptr && c.epoch != nullptr) {
-    int slot = page;
-    if (cache.pages > DG_MAX_B) {  // the request whose first row this is, plus 1
-      uint32_t r = 0;
-      for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
-        if (c.start[i] == row0 && c.start[i + 1] > row0) r = i + 1;
-      }
-      slot = static_cast<int>(block_check(r, 0, sums).x) - 1;
+constexpr int kAppendThreads = DG_PAGE * kDim / 16 / kMine;
+static_assert(kAppendThreads<64> >= kAppendHeads, "a thread for each head's mark");
+
+// The tags and the codes put aside of a run's heads, from head 0 on; tags null:
+// nothing is put aside.  All threads of the block.
+struct KeptPlace {
+  KeptTag* tags;
+  uint32_t* codes;
+  uint32_t epoch;
+};
+template <int kDim>
+DG_DEV KeptPlace kept_place(const dg_context& c, const dg_context_cache& cache, bool is_k, int page, int row0, uint32_t* sums) {
+  KeptPlace k = {nullptr, nullptr, 0};
+  if (cache.kept == nullptr || c.epoch == nullptr) return k;
+  int slot = page;
+  if (cache.pages > DG_MAX_B) {  // the request whose first row this is
+    uint32_t r = 0;
+    for (int i = threadIdx.x; i < c.B; i += blockDim.x) {
+      if (c.start[i] == row0 && c.start[i + 1] > row0) r = i + 1;
     }
-    if (slot >= 0 && slot < DG_MAX_B) {
-      const KeptLayout l = kept_layout(cache.pages, cache.heads, kDim);
-      const size_t at = (static_cast<size_t>(slot) * 2 + (is_k ? 0 : 1)) * cache.heads + h;
-      tag = reinterpret_cast<KeptTag*>(cache.kept + l.tags) + at;
-      kept = reinterpret_cast<uint32_t*>(cache.kept + l.codes + at * DG_PAGE * kDim);
-      epoch = static_cast<uint32_t>(*c.epoch);
-    }
+    slot = static_cast<int>(block_check(r, 0, sums).x) - 1;
+    if (slot < 0 || slot >= DG_MAX_B) return k;
   }
+  const KeptLayout l = kept_layout(cache.pages, cache.heads, kDim);
+  const size_t at = (static_cast<size_t>(slot) * 2 + (is_k ? 0 : 1)) * cache.heads;
+  k.tags = reinterpret_cast<KeptTag*>(cache.kept + l.tags) + at;
+  k.codes = reinterpret_cast<uint32_t*>(cache.kept + l.codes + at * DG_PAGE * kDim);
+  k.epoch = static_cast<uint32_t>(*c.epoch);
+  return k;
+}
+
+// One head of a run behind held tokens whose scale the new rows want to be `s`,
+// where that is above the page's, or where the page's has grown before: the
+// held codes under the scale that comes of it, that scale, and the rows' codes.
+// By a block, or (kBlock false) by a warp.
+template <int kDim, bool kBlock>
+DG_DEV void append_grown_head(const dg_context_cache& cache, const dg_heads& in, uint32_t* marks, const float2 (*turns)[kDim / 2], int rot16,
+                              bool il, bool is_k, int4 run, int h, float s, const KeptPlace& k, uint32_t* sums) {
+  constexpr int kUnits = kDim / 16, kTeam = kBlock ? kAppendThreads<kDim> : 32;
+  constexpr int kAtOnce = 8;  // words on their way: all that a block has of a page
+  const int t = kBlock ? threadIdx.x : (threadIdx.x & 31);
+  const int page = run.x, row0 = run.y, off = run.z, n = run.w;
+  const size_t at = static_cast<size_t>(page) * cache.heads + h;
+  uint8_t* page_codes = (is_k ? cache.k : cache.v) + at * DG_PAGE * kDim;
+  uint32_t* codes = reinterpret_cast<uint32_t*>(page_codes);
+  float* scale = (is_k ? cache.k_scale : cache.v_scale) + at;
+  KeptTag* tag = k.tags == nullptr ? nullptr : k.tags + h;
+  uint32_t* kept = k.codes + static_cast<size_t>(h) * (DG_PAGE * kDim / 4);
+  const int words = off * kDim / 4;
+  auto check = [&](uint32_t a, uint32_t b) {  // over the team, every thread past what it read before
+    if (kBlock) return block_check(a, b, sums);
+    return make_uint2(__reduce_add_sync(0xffffffffu, a), __reduce_add_sync(0xffffffffu, b));
+  };
+  const float old = *scale;
   bool mine = false, restore = false;  // the tag is of this page as it stands: of this plan's batch, or of another's
   float base = old;
-  if (tag != nullptr && tag->page == page && tag->off == off && __float_as_uint(tag->grown) == __float_as_uint(old) &&
-      (s > old || tag->epoch != epoch)) {
-    uint32_t a = 0, b = 0;
-    for (int i = threadIdx.x; i < words; i += blockDim.x) check_word(i, codes[i], a, b);
-    const uint2 sum = block_check(a, b, sums);
+  uint32_t a = 0, b = 0;
+  if (tag != nullptr && tag->page == page && tag->off == off && __float_as_uint(tag->grown) == __float_as_uint(old)) {
+    for (int i0 = t; i0 < words; i0 += kAtOnce * kTeam) {
+      uint32_t w[kAtOnce];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) w[j] = i0 + j * kTeam < words ? codes[i0 + j * kTeam] : 0u;
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        if (i0 + j * kTeam < words) check_word(i0 + j * kTeam, w[j], a, b);
+      }
+    }
+    const uint2 sum = check(a, b);
     const bool same = sum.x == tag->check[0] && sum.y == tag->check[1];
-    mine = same && tag->epoch == epoch;
+    mine = same && tag->epoch == k.epoch;
     restore = same && !mine;
     if (restore) base = tag->base;
   }
   const bool grows = s > base;
-  if (!grows && !restore) return old;
-  const float ratio = base / s;
-  uint32_t a = 0, b = 0;
-  for (int i = threadIdx.x; i < words; i += blockDim.x) {
-    uint32_t w = restore ? kept[i] : codes[i];
-    if (grows) {
-      if (tag != nullptr && !mine && !restore) kept[i] = w;
-      float f[4];
+  if (!grows) s = base;
+  a = b = 0;
+  if (grows || restore) {
+    const float ratio = base / s;
+    const uint32_t* from = restore ? kept : codes;
+    for (int i0 = t; i0 < words; i0 += kAtOnce * kTeam) {
+      uint32_t w[kAtOnce];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const __half_raw hr = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(w >> (8 * j)), __NV_E4M3);
-        f[j] = __half2float(*reinterpret_cast<const __half*>(&hr)) * ratio;
-      }
-      w = e4m3_pair(f[0], f[1]) | e4m3_pair(f[2], f[3]) << 16;
-    }
-    codes[i] = w;
-    check_word(i, w, a, b);
-  }
-  if (tag != nullptr) {
-    const uint2 sum = block_check(a, b, sums);
-    if (threadIdx.x == 0) {
-      if (grows) {
-        if (!mine) {
-          tag->page = page;
-          tag->off = off;
-          tag->epoch = epoch;
-          tag->base = base;
+      for (int j = 0; j < kAtOnce; ++j) w[j] = i0 + j * kTeam < words ? from[i0 + j * kTeam] : 0u;
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int i = i0 + j * kTeam;
+        if (i >= words) continue;
+        if (grows) {
+          if (tag != nullptr && !mine && !restore) kept[i] = w[j];
+          float f[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const __half_raw hr = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(w[j] >> (8 * e)), __NV_E4M3);
+            f[e] = __half2float(*reinterpret_cast<const __half*>(&hr)) * ratio;
+          }
+          w[j] = e4m3_pair(f[0], f[1]) | e4m3_pair(f[2], f[3]) << 16;
         }
-        tag->grown = s;
-        tag->check[0] = sum.x;
-        tag->check[1] = sum.y;
-        cache.kept[page] = static_cast<uint8_t>(off);  // by every head that grows: the same
-      } else {
-        tag->off = 0;  // the page is as it was
+        codes[i] = w[j];
+        check_word(i, w[j], a, b);
       }
     }
   }
-  return grows ? s : base;
-}
-
-constexpr int kMine = 2;
-template <int kDim>
-constexpr int kAppendThreads = DG_PAGE * kDim / 16 / kMine;
-
-// The heads that want[h] > 0 names, of a run behind held tokens: the scale that
-// the rows want is above the page's, or the page's has grown before.  All threads
-// of the block.  Out of line and on its own: within the loop over the heads its
-// registers cost every append (256 requests x 8 heads x 1 row 12.9 us instead of 12.0).
-template <int kDim>
-__device__ __noinline__ void append_grown(const dg_context& c, const dg_context_cache& cache, const dg_heads& in,
-                                          const float2 (*turns)[kDim / 2], int rot16, bool il, bool is_k, int4 run,
-                                          int head0, int heads, const float* want, uint32_t* sums) {
-  constexpr int kUnits = kDim / 16, kRows = kAppendThreads<kDim> / kUnits;
-  const int page = run.x, row0 = run.y, off = run.z, n = run.w;
-  const int u = threadIdx.x % kUnits;
+  const uint2 sum = check(a, b);
+  if (t == 0) {
+    *scale = s;
+    if (tag != nullptr && grows) {
+      if (!mine) {
+        tag->page = page;
+        tag->off = off;
+        tag->epoch = k.epoch;
+        tag->base = base;
+      }
+      tag->grown = s;
+      tag->check[0] = sum.x;
+      tag->check[1] = sum.y;
+      marks[at] = grown_mark(k.epoch, off);
+    } else if (tag != nullptr) {  // as it was, or written by somebody else
+      tag->off = 0;
+      marks[at] = 0;
+    }
+  }
+  const float inv = 1.0f / s;  // exact: a power of two
+  const int u = t % kUnits;
   int ca, cb;
   unit_chunks(u, rot16, il, ca, cb);
-  for (int h = head0; h < head0 + heads; ++h) {
-    if (!(want[h - head0] > 0.f)) continue;
-    const size_t at = static_cast<size_t>(page) * cache.heads + h;
-    float* scale = (is_k ? cache.k_scale : cache.v_scale) + at;
-    const float old = *scale;
-    __syncthreads();  // everybody has read it
-    const float s = settle_kept<kDim>(c, cache, is_k, h, page, row0, off, old, want[h - head0], sums);
-    const float inv = 1.0f / s;  // exact: a power of two
-    uint8_t* codes = (is_k ? cache.k : cache.v) + (at * DG_PAGE + off) * kDim;
-    for (int row = threadIdx.x / kUnits; row < n; row += kRows) {
-      const uint8_t* src = static_cast<const uint8_t*>(in.data) + 2 * ((row0 + row) * in.row_stride + h * in.head_stride);
-      float a[8], b[8];
-      unpack8(*reinterpret_cast<const uint4*>(src + 16 * ca), a);
-      unpack8(*reinterpret_cast<const uint4*>(src + 16 * cb), b);
+  constexpr int kRows = kTeam / kUnits;
+  const uint8_t* src = static_cast<const uint8_t*>(in.data) + 2 * h * in.head_stride;
+  for (int r0 = t / kUnits; r0 < n; r0 += kMine * kRows) {
+    uint4 wa[kMine], wb[kMine];
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+      const uint8_t* row = src + 2 * (row0 + min(r0 + m * kRows, n - 1)) * in.row_stride;
+      wa[m] = *reinterpret_cast<const uint4*>(row + 16 * ca);
+      wb[m] = *reinterpret_cast<const uint4*>(row + 16 * cb);
+    }
+#pragma unroll
+    for (int m = 0; m < kMine; ++m) {
+      const int row = r0 + m * kRows;
+      if (row >= n) continue;
+      float x[8], y[8];
+      unpack8(wa[m], x);
+      unpack8(wb[m], y);
       if (u < rot16) {
         float2 tr[8];
         read_turns(turns[row], u, rot16, tr);
-        rotate_unit(a, b, tr, il);
+        rotate_unit(x, y, tr, il);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        if (a[j] != a[j]) a[j] = 0.f;
-        if (b[j] != b[j]) b[j] = 0.f;
+      for (int j = 0; j < 8; ++j) {  // NaN becomes 0
+        if (x[j] != x[j]) x[j] = 0.f;
+        if (y[j] != y[j]) y[j] = 0.f;
       }
-      *reinterpret_cast<uint2*>(codes + row * kDim + 8 * ca) = e4m3_chunk(a, inv);
-      *reinterpret_cast<uint2*>(codes + row * kDim + 8 * cb) = e4m3_chunk(b, inv);
+      uint8_t* dst = page_codes + (off + row) * kDim;
+      *reinterpret_cast<uint2*>(dst + 8 * ca) = e4m3_chunk(x, inv);
+      *reinterpret_cast<uint2*>(dst + 8 * cb) = e4m3_chunk(y, inv);
     }
-    if (threadIdx.x == 0) *scale = s;
+  }
+}
+
+// The heads of a list, each with the scale that its rows want.  All threads of
+// the block: a head after the other, or, of many, a warp to each.  Out of line
+// and on its own: within the loop over the heads its registers cost every append
+// (256 requests x 8 heads x 1 row 12.9 us instead of 12.4).
+struct GrownHead {
+  int head;
+  float want;
+};
+template <int kDim>
+__device__ __noinline__ void append_grown(const dg_context& c, const dg_context_cache& cache, const dg_heads& in,
+                                          const float2 (*turns)[kDim / 2], int rot16, bool il, bool is_k, int4 run,
+                                          const GrownHead* list, int count, uint32_t* sums) {
+  const KeptPlace k = kept_place<kDim>(c, cache, is_k, run.x, run.y, sums);
+  uint32_t* marks = reinterpret_cast<uint32_t*>(cache.kept) + (is_k ? 0 : static_cast<size_t>(cache.pages) * cache.heads);
+  if (count <= 2) {
+    for (int i = 0; i < count; ++i)
+      append_grown_head<kDim, true>(cache, in, marks, turns, rot16, il, is_k, run, list[i].head, list[i].want, k, sums);
+  } else {
+    for (int i = threadIdx.x >> 5; i < count; i += blockDim.x >> 5)
+      append_grown_head<kDim, false>(cache, in, marks, turns, rot16, il, is_k, run, list[i].head, list[i].want, k, sums);
   }
 }
 
@@ -630,8 +687,8 @@ context_append_kernel(const __grid_constant__ dg_context c, const __grid_constan
   __shared__ float s_top[3][kWarps];
   __shared__ __align__(16) float2 s_turn[DG_PAGE][kDim / 2];
   __shared__ uint32_t s_check[2 * kWarps];
-  __shared__ float s_want[1024];  // the scales wanted by heads that append_grown is to do
-  __shared__ bool s_grown;
+  __shared__ uint32_t s_bits[kAppendHeads / 32];
+  __shared__ GrownHead s_grown[kAppendHeads];
   wait_for_previous_kernel();
   allow_next_kernel();
   const int4 run = reinterpret_cast<const int4*>(c.runs)[blockIdx.x];
@@ -662,11 +719,14 @@ context_append_kernel(const __grid_constant__ dg_context c, const __grid_constan
     }
   };
   load(src);
-  // Did some head's scale grow with this page at this many held tokens?  One
-  // thread asks, for all to see the same: other blocks may be writing it.
-  int grown_at = 0;
-  if (threadIdx.x == 0 && off > 0 && cache.kept != nullptr) grown_at = cache.kept[page];
-  bool later = false;
+  // heads whose scale another plan's batch behind the same tokens has made to grow
+  bool grown = false;
+  if (off > 0 && static_cast<int>(threadIdx.x) < heads && cache.kept != nullptr && c.epoch != nullptr) {
+    const uint32_t* marks = reinterpret_cast<const uint32_t*>(cache.kept) + (is_k ? 0 : static_cast<size_t>(cache.pages) * cache.heads);
+    const uint32_t m = marks[at0 + threadIdx.x], now = grown_mark(static_cast<uint32_t>(*c.epoch), off);
+    grown = m != now && (m & (DG_PAGE - 1)) == (now & (DG_PAGE - 1));
+  }
+  int later = 0;  // heads for append_grown
   if (rot16 > 0) {
     const int half = 8 * rot16, stride = kThreads / half;
     const int j = threadIdx.x % half;  // this thread's frequency; the block's threads walk the rows
@@ -715,7 +775,10 @@ context_append_kernel(const __grid_constant__ dg_context c, const __grid_constan
       top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(s_top[buffer][threadIdx.x & (kWarps - 1)])));
     };
     if (zero != zero) top = INFINITY;
-    if (threadIdx.x == 0 && h == 0) s_grown = grown_at == off;
+    if (h == 0 && threadIdx.x < kAppendHeads) {
+      const uint32_t bits = __ballot_sync(0xffffffffu, grown);
+      if ((threadIdx.x & 31) == 0) s_bits[threadIdx.x >> 5] = bits;
+    }
     largest(h & 1);
     if (top > FLT_MAX) {  // seldom: what is not finite does not count, NaN becomes 0
       top = 0.f;
@@ -737,13 +800,9 @@ context_append_kernel(const __grid_constant__ dg_context c, const __grid_constan
     const int e = scale_exponent(top);
     float s = power_of_two(e), inv = power_of_two(-e);  // |e| <= 120
     if (off > 0) {
-      if (s > old || s_grown) {
-        if (!later) {
-          for (int i = threadIdx.x; i < heads; i += kThreads) s_want[i] = 0.f;
-          __syncthreads();
-        }
-        later = true;
-        if (threadIdx.x == 0) s_want[h] = s;
+      if (s > old || (s_bits[h >> 5] >> (h & 31) & 1u)) {
+        if (threadIdx.x == 0) s_grown[later] = GrownHead{head0 + h, s};
+        ++later;
         continue;
       }
       s = old;
@@ -758,9 +817,9 @@ context_append_kernel(const __grid_constant__ dg_context c, const __grid_constan
     }
     if (threadIdx.x == 0) *scale = s;
   }
-  if (later) {
+  if (later > 0) {
     __syncthreads();
-    append_grown<kDim>(c, cache, in, s_turn, rot16, il, is_k, run, head0, heads, s_want, s_check);
+    append_grown<kDim>(c, cache, in, s_turn, rot16, il, is_k, run, s_grown, later, s_check);
   }
 }
 
@@ -936,7 +995,7 @@ dg_status dg_context_append(const dg_context* ctx, const dg_context_cache* cache
   // 5.4 / 8.0; 16 x 256 11.8 / 9.3 / 8.3 / 10.7; 32 x 256 19.9 / 14.8 / 12.8 / 12.2.
   const int runs = DG_CONTEXT_RUNS(ctx->rows, ctx->B);
   int per = 1;
-  while (per < cache->heads && 4ll * runs * ((cache->heads + per - 1) / per) > 7ll * sms) per *= 2;
+  while (per < cache->heads && per < kAppendHeads && 4ll * runs * ((cache->heads + per - 1) / per) > 7ll * sms) per *= 2;
   const dim3 grid(runs, (cache->heads + per - 1) / per, 2);
   auto kernel = cache->dim == 128 ? context_append_kernel<128> : context_append_kernel<64>;
   const cudaError_t e = launch_context(kernel, grid, cache->dim * (DG_PAGE / 16) / kMine, 0, static_cast<cudaStream_t>(stream),

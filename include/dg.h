@@ -498,7 +498,7 @@ typedef struct {
 } dg_context_cache;
 
 /* Bytes of dg_context_cache.kept (0 if invalid): room for the codes of
- * min(pages, DG_MAX_B) pages, and a byte for every page. */
+ * min(pages, DG_MAX_B) pages, and a word beside every scale. */
 size_t dg_context_kept_size(int32_t pages, int32_t heads, int32_t dim);
 
 /* dg_context_append -- keys and values of the batch's rows into their slots.
