@@ -8,6 +8,7 @@ raise ``DGError``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import itertools
 import os
@@ -221,6 +222,14 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+def _allocating_on(stream):
+    """Tensors made within belong to ``stream`` (None: the current one), where
+    the call that fills them runs: memory of another stream's may still be in
+    use there."""
+    import torch
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _host(a, dtype) -> np.ndarray:
     return np.ascontiguousarray(np.asarray(a, dtype=dtype))
 
@@ -250,7 +259,8 @@ class Workspace:
         if n == 0:
             raise DGError(2, "workspace_size")
         self.nbytes = n
-        self.buf = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+        with _allocating_on(stream):
+            self.buf = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
         _check(lib().dg_workspace_init(_ptr(self.buf), ctypes.c_size_t(n), _stream(stream)),
                "dg_workspace_init")
 
@@ -714,10 +724,13 @@ class RopeFrequencies:
 
 def rope(x, positions, frequencies: RopeFrequencies, out=None, stream=None):
     """Rotary positions (``dg_rope``): bfloat16 ``x`` [rows, heads, dim], int32
-    ``positions`` [rows]; returns ``out`` (``x`` itself for in place)."""
+    ``positions`` [rows]; returns ``out`` (``x`` itself for in place).  None: a new
+    tensor, one of ``stream``'s, whose rows without a position are 0."""
     import torch
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+        _need(stream is None or stream.device == x.device, "the stream belongs to another device than the tensors")
+        with _allocating_on(stream):
+            out = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
     _need(x.dim() == 3, "x must be [rows, heads, dim]")
     rows, heads, dim = x.shape
     _need(positions.dtype == torch.int32 and positions.dim() == 1 and positions.is_contiguous() and
@@ -777,17 +790,20 @@ def context_workspace_size(rows: int, q_heads: int, kv_heads: int, dim: int) -> 
 
 class ContextWorkspace:
     """Device scratch of ``context_attention`` for one shape (a zeroed torch
-    uint8 buffer; ``device_status`` reads its fault latch)."""
+    uint8 buffer, one of ``stream``'s; ``device_status`` reads its fault latch)."""
 
     def __init__(self, rows: int, q_heads: int, kv_heads: int, dim: int, device=None, stream=None):
         import torch
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        _need(stream is None or device.index is None or stream.device == device,
+              "the stream belongs to another device than the workspace")
         with torch.cuda.device(device):
             n = context_workspace_size(rows, q_heads, kv_heads, dim)
             if n == 0:
                 raise DGError(2, "context_workspace_size")
             self.nbytes = n
-            self.buf = torch.empty(n, dtype=torch.uint8, device=device)
+            with _allocating_on(stream):
+                self.buf = torch.empty(n, dtype=torch.uint8, device=device)
             _check(lib().dg_workspace_init(_ptr(self.buf), ctypes.c_size_t(n), _stream(stream)), "dg_workspace_init")
 
 
@@ -822,8 +838,9 @@ def debug_gumbel(words, stream=None):
     for uint32 words (torch int32 CUDA tensor)."""
     import torch
     n = int(words.numel())
-    g = torch.empty(n, dtype=torch.float32, device=words.device)
-    a = torch.empty(n, dtype=torch.float32, device=words.device)
+    with _allocating_on(stream):
+        g = torch.empty(n, dtype=torch.float32, device=words.device)
+        a = torch.empty(n, dtype=torch.float32, device=words.device)
     _check(lib().dg_debug_gumbel(_ptr(words), ctypes.c_int32(n), _ptr(g), _ptr(a), _stream(stream)),
            "dg_debug_gumbel")
     return g, a
