@@ -549,7 +549,8 @@ def generate_blocks_context(plan: ContextPlan, E, hidden_fn, n_blocks: int, h_bu
     first.  After block j's last step ``hidden_fn(j, params.max_steps, canvas,
     committed, h_buf)`` is called once more, with the finished canvas, to encode
     it: what it appends then is what the next plan commits (``h_buf`` is not
-    read)."""
+    read).  DGError 10 when a block does not fit, 9 when a key or value that is
+    not finite was appended."""
     return _run_blocks(plan, E, hidden_fn, n_blocks, h_buf, blocks, canvas, prev_argmax, accept, entropy, sampled,
                        argmax, stop, ws, params, e_scale, stream)
 
@@ -696,8 +697,9 @@ def context_plan(plan: ContextPlan, add, release=None, commit: bool = False, str
 
 
 def context_status(plan: ContextPlan, stream=None) -> int:
-    """Synchronise and report (``dg_context_status``): 0, 10 (the last batch
-    was refused) or 9 (an append met a value that is not finite; cleared)."""
+    """Synchronise and report (``dg_context_status``): 10 (the last batch was
+    refused), else 9 (an append met a value that is not finite; cleared by this
+    answer), else 0."""
     import torch
     with torch.cuda.device(plan.device):
         return int(lib().dg_context_status(plan._ref, _stream(stream)))

@@ -135,6 +135,8 @@ dg_status run_blocks(const dg_shape* shape, const dg_params* params, const void*
     // the batch is still provisional
     if (ctx != nullptr && block_trampoline(params->max_steps, canvas, h_buf, &call, stream) != 0)
       return call.status != DG_OK ? call.status : DG_ERR_CALLBACK;
+    // a key or value of this block that is not finite, before anything commits it
+    if (ctx != nullptr && (st = dg_context_status(ctx, stream)) != DG_OK) return st;
   }
   if (cudaStreamSynchronize(cs) != cudaSuccess) return DG_ERR_CUDA;
   return DG_OK;

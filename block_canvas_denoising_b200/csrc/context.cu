@@ -894,15 +894,14 @@ dg_status dg_context_status(const dg_context* ctx, void* stream) {
   if (!cuda_ok(cudaMemcpyAsync(s, ctx->status, sizeof(s), cudaMemcpyDeviceToHost, cs), "context status read") ||
       !cuda_ok(cudaStreamSynchronize(cs), "stream synchronise"))
     return DG_ERR_CUDA;
-  if (s[1] != 0 && !cuda_ok(cudaMemsetAsync(ctx->status + 1, 0, sizeof(int32_t), cs), "context latch clear"))
-    return DG_ERR_CUDA;
   if (s[0] != 0) {
     set_last_error_message(s[0] == 1   ? "the context's pool has too few free pages for the batch"
                            : s[0] == 2 ? "the batch has more rows than the context"
                                        : "a length is negative or beyond the context's table");
     return DG_ERR_CAPACITY;
   }
-  if (s[1] != 0) {
+  if (s[1] != 0) {  // reported, so it may go
+    if (!cuda_ok(cudaMemsetAsync(ctx->status + 1, 0, sizeof(int32_t), cs), "context latch clear")) return DG_ERR_CUDA;
     set_last_error_message("a key or value appended to the context is not finite");
     return DG_ERR_VALUE;
   }

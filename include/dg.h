@@ -437,9 +437,9 @@ dg_status dg_context_plan(const dg_context* ctx, const int32_t* add, const uint8
                           void* stream);
 
 /* Synchronise `stream` and report the context: DG_ERR_CAPACITY when the last
- * plan was refused (the reason in dg_last_error_message()), DG_ERR_VALUE when
- * an append met a value that is not finite since the last call (the latch is
- * cleared), else DG_OK. */
+ * plan was refused (the reason in dg_last_error_message()), else DG_ERR_VALUE
+ * when an append met a value that is not finite since a call last said so (the
+ * latch is cleared by this answer only), else DG_OK. */
 dg_status dg_context_status(const dg_context* ctx, void* stream);
 
 /* A bf16 tensor [rows][heads][dim] on the device: dim contiguous, strides in
@@ -564,7 +564,10 @@ dg_status dg_context_attention(const dg_context* ctx, const dg_context_cache* ca
  * device buffer that the call fills.  A batch planned before the call (the
  * prompts) is committed by block 0's plan; the last block, encoded too, stays
  * provisional.
- * DG_ERR_CAPACITY when a block does not fit. */
+ * DG_ERR_CAPACITY when a block does not fit; DG_ERR_VALUE when a key or value
+ * that is not finite was appended: by the prompts (before block 0's first step)
+ * or during a block (after its encoding: the block is in `blocks`, and not
+ * committed to the context). */
 dg_status dg_generate_blocks_context(const dg_shape* shape, const dg_params* params, const void* E,
                                      const float* e_scale, int32_t n_blocks, dg_block_hidden_fn hidden_fn,
                                      void* user, const dg_context* ctx, int32_t* add, void* h_buf,
