@@ -551,8 +551,15 @@ def generate_blocks_context(plan: ContextPlan, E, hidden_fn, n_blocks: int, h_bu
     it: what it appends then is what the next plan commits (``h_buf`` is not
     read).  DGError 10 when a block does not fit, 9 when a key or value that is
     not finite was appended."""
-    return _run_blocks(plan, E, hidden_fn, n_blocks, h_buf, blocks, canvas, prev_argmax, accept, entropy, sampled,
-                       argmax, stop, ws, params, e_scale, stream)
+    import torch
+    given = dict(E=E, h_buf=h_buf, blocks=blocks, canvas=canvas, prev_argmax=prev_argmax, accept=accept, entropy=entropy,
+                 sampled=sampled, argmax=argmax, stop=stop, workspace=ws.buf, e_scale=e_scale)
+    for name, t in given.items():
+        _need(t is None or t.device == plan.device, f"{name} is on another device than the plan, {plan.device}")
+    _need(stream is None or stream.device == plan.device, "the stream belongs to another device than the plan")
+    with torch.cuda.device(plan.device):
+        return _run_blocks(plan, E, hidden_fn, n_blocks, h_buf, blocks, canvas, prev_argmax, accept, entropy, sampled,
+                           argmax, stop, ws, params, e_scale, stream)
 
 
 def _run_blocks(plan, E, hidden_fn, n_blocks, h_buf, blocks, canvas, prev_argmax, accept, entropy, sampled, argmax,
