@@ -222,10 +222,10 @@ def _stream(stream) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
-def _allocating_on(stream):
-    """Tensors made within belong to ``stream`` (None: the current one), where
-    the call that fills them runs: memory of another stream's may still be in
-    use there."""
+def _on(stream):
+    """``stream`` (None: the current one) is the current stream within.  Tensors
+    made there belong to it, as the call that fills them does (memory of another
+    stream's may still be in use there), and so does what a callback launches."""
     import torch
     return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
@@ -259,7 +259,7 @@ class Workspace:
         if n == 0:
             raise DGError(2, "workspace_size")
         self.nbytes = n
-        with _allocating_on(stream):
+        with _on(stream):
             self.buf = torch.empty(n, dtype=torch.uint8, device=device or "cuda")
         _check(lib().dg_workspace_init(_ptr(self.buf), ctypes.c_size_t(n), _stream(stream)),
                "dg_workspace_init")
@@ -357,7 +357,7 @@ def denoise_loop(E, hidden_fn, h_buf, canvas, prev_argmax, has_prev, accept, ent
     """Run the adaptive loop (``dg_denoise_loop``).
 
     ``hidden_fn(k, canvas_tensor, h_buf)`` must fill ``h_buf`` for step k on
-    the current stream and return None.  ``has_prev`` is a host uint8 numpy
+    the current stream (``stream``, if one is given) and return None.  ``has_prev`` is a host uint8 numpy
     array [B] updated in place.  Returns the host int32 array of steps taken.
     """
     B = int(len(has_prev))
@@ -379,12 +379,13 @@ def denoise_loop(E, hidden_fn, h_buf, canvas, prev_argmax, has_prev, accept, ent
             return 1
 
     cfn = _HIDDEN_FN(cb)
-    code = lib().dg_denoise_loop(
-        ctypes.byref(shp), ctypes.byref(prm), _ptr(E), _ptr(e_scale), cfn, None,
-        ctypes.c_int32(k_start), _ptr(h_buf), _ptr(canvas), _ptr(prev_argmax),
-        has_prev.ctypes.data_as(ctypes.c_void_p), steps.ctypes.data_as(ctypes.c_void_p),
-        _ptr(accept), _ptr(entropy), _ptr(sampled), _ptr(argmax), _ptr(stop), _ptr(ws.buf),
-        ctypes.c_size_t(ws.nbytes), _stream(stream))
+    with _on(stream):
+        code = lib().dg_denoise_loop(
+            ctypes.byref(shp), ctypes.byref(prm), _ptr(E), _ptr(e_scale), cfn, None,
+            ctypes.c_int32(k_start), _ptr(h_buf), _ptr(canvas), _ptr(prev_argmax),
+            has_prev.ctypes.data_as(ctypes.c_void_p), steps.ctypes.data_as(ctypes.c_void_p),
+            _ptr(accept), _ptr(entropy), _ptr(sampled), _ptr(argmax), _ptr(stop), _ptr(ws.buf),
+            ctypes.c_size_t(ws.nbytes), _stream(stream))
     if code != 0:
         err = DGError(code, "dg_denoise_loop")
         if errors:
@@ -531,7 +532,8 @@ def generate_blocks(E, hidden_fn, n_blocks: int, h_buf, blocks, canvas, prev_arg
     """Block-by-block generation (``dg_generate_blocks``).
 
     ``hidden_fn(j, k, canvas_tensor, committed, h_buf)`` fills ``h_buf``
-    for step k of block j on the current stream; ``committed`` is the view
+    for step k of block j on the current stream (``stream``, if one is given);
+    ``committed`` is the view
     ``blocks[:j]`` of the blocks committed so far.  ``blocks`` is an int32
     CUDA tensor [n_blocks, B*256].  Returns the host int32 array of steps
     taken, [n_blocks, B]."""
@@ -586,12 +588,13 @@ def _run_blocks(plan, E, hidden_fn, n_blocks, h_buf, blocks, canvas, prev_argmax
     tail = (_ptr(h_buf), _ptr(blocks), steps.ctypes.data_as(ctypes.c_void_p), _ptr(canvas), _ptr(prev_argmax),
             _ptr(accept), _ptr(entropy), _ptr(sampled), _ptr(argmax), _ptr(stop), _ptr(ws.buf),
             ctypes.c_size_t(ws.nbytes), _stream(stream))
-    if plan is None:
-        where = "dg_generate_blocks"
-        code = lib().dg_generate_blocks(*head, *tail)
-    else:
-        where = "dg_generate_blocks_context"
-        code = lib().dg_generate_blocks_context(*head, plan._ref, _ptr(plan.add), *tail)
+    with _on(stream):
+        if plan is None:
+            where = "dg_generate_blocks"
+            code = lib().dg_generate_blocks(*head, *tail)
+        else:
+            where = "dg_generate_blocks_context"
+            code = lib().dg_generate_blocks_context(*head, plan._ref, _ptr(plan.add), *tail)
     if code != 0:
         err = DGError(code, where)
         if errors:
@@ -738,7 +741,7 @@ def rope(x, positions, frequencies: RopeFrequencies, out=None, stream=None):
     import torch
     if out is None:
         _need(stream is None or stream.device == x.device, "the stream belongs to another device than the tensors")
-        with _allocating_on(stream):
+        with _on(stream):
             out = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
     _need(x.dim() == 3, "x must be [rows, heads, dim]")
     rows, heads, dim = x.shape
@@ -811,7 +814,7 @@ class ContextWorkspace:
             if n == 0:
                 raise DGError(2, "context_workspace_size")
             self.nbytes = n
-            with _allocating_on(stream):
+            with _on(stream):
                 self.buf = torch.empty(n, dtype=torch.uint8, device=device)
             _check(lib().dg_workspace_init(_ptr(self.buf), ctypes.c_size_t(n), _stream(stream)), "dg_workspace_init")
 
@@ -847,7 +850,7 @@ def debug_gumbel(words, stream=None):
     for uint32 words (torch int32 CUDA tensor)."""
     import torch
     n = int(words.numel())
-    with _allocating_on(stream):
+    with _on(stream):
         g = torch.empty(n, dtype=torch.float32, device=words.device)
         a = torch.empty(n, dtype=torch.float32, device=words.device)
     _check(lib().dg_debug_gumbel(_ptr(words), ctypes.c_int32(n), _ptr(g), _ptr(a), _stream(stream)),

@@ -64,3 +64,48 @@ def test_rope_rows_without_a_position_of_a_new_tensor_are_zero():
         out = dg.rope(x, pos, f, stream=stream)
         torch.cuda.synchronize()
         assert (out[::3] == 0).all() and out[1::3].abs().max() > 0
+
+
+def test_a_producer_runs_on_the_stream_of_its_steps():
+    # it fills h late: steps that did not wait would read the call before's
+    import numpy as np
+    import synth
+    from dg_testlib import to_dev_bf16
+    L, B, D, V, n_blocks = 256, 1, 256, 1024, 2
+    R = L * B
+    E_bits = synth.embedder_normal(V, D, seed=1)
+    E = to_dev_bf16(E_bits)
+    y = synth.loop_targets(L, V, seed=3, B=B)
+    table = [to_dev_bf16(synth.loop_hidden(k, y, E_bits, seed=4)) for k in range(49)]
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+
+    def run(name, stream):
+        h = torch.zeros((R, D), dtype=torch.bfloat16, device="cuda")
+        blocks, canvas = i32(n_blocks, R), i32(R)
+        late = stream is not None
+
+        def hidden(*args):
+            k = args[0] if name == "loop" else args[1]
+            if late:
+                assert torch.cuda.current_stream() == stream
+                torch.cuda._sleep(3_000_000)
+            h.copy_(table[k])
+        outs = (torch.zeros(R, dtype=torch.uint8, device="cuda"), torch.zeros(R, dtype=torch.float32, device="cuda"), i32(R),
+                i32(R), i32(B), dg.Workspace(B, D, V))
+        torch.cuda.synchronize()
+        if name == "loop":
+            steps = dg.denoise_loop(E, hidden, h, canvas, i32(R), np.zeros(B, np.uint8), *outs, stream=stream)
+            result = canvas
+        else:
+            args = (E, hidden, n_blocks, h, blocks, canvas, i32(R), *outs)
+            if name == "context":
+                steps = dg.generate_blocks_context(dg.ContextPlan(B, R, 20, 10), *args, stream=stream)
+            else:
+                steps = dg.generate_blocks(*args, stream=stream)
+            result = blocks
+        torch.cuda.synchronize()
+        return steps, result
+    for name in ("loop", "blocks", "context"):
+        want = run(name, None)
+        got = run(name, torch.cuda.Stream())
+        assert np.array_equal(want[0], got[0]) and torch.equal(want[1], got[1]), name
