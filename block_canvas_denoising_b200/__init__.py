@@ -620,6 +620,12 @@ def _need(ok: bool, what: str) -> None:
         raise DGError(1, what)
 
 
+def _need_int32(**sizes) -> None:
+    """ctypes would take the low 32 bits of a number that is too large."""
+    for name, n in sizes.items():
+        _need(-2 ** 31 <= n < 2 ** 31, f"{name} = {n} is beyond 32 bits")
+
+
 def _call(device, fn, where, stream, *args):
     """Call a library function on ``stream`` (None: the current one) with the
     tensors' device current."""
@@ -668,6 +674,7 @@ class ContextPlan:
     def __init__(self, B: int, rows: int, pages: int, max_pages: int, device=None):
         import torch
         _need(min(B, rows, pages, max_pages) >= 1, "ContextPlan sizes must be positive")
+        _need_int32(B=B, rows=rows, pages=pages, max_pages=max_pages)
         device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         if device.type == "cuda" and device.index is None:
             device = torch.device("cuda", torch.cuda.current_device())
@@ -724,6 +731,7 @@ class RopeFrequencies:
                  original_length: int = 4096, interleaved: bool = False, device=None):
         import torch
         _need(scaling in _ROPE_SCALING, f"scaling must be one of {sorted(_ROPE_SCALING)}")
+        _need_int32(rot=rot, original_length=original_length)
         f = np.zeros(max(int(rot), 2) // 2, np.float64)
         mag = ctypes.c_float()
         _check(lib().dg_rope_frequencies(rot, base, _ROPE_SCALING[scaling], factor, original_length,
@@ -768,6 +776,7 @@ class ContextCache:
         import torch
         device = "cuda" if device is None else device
         _need(min(pages, heads, dim) >= 1, "ContextCache sizes must be positive")
+        _need_int32(pages=pages, heads=heads, dim=dim)
         self.pages, self.heads, self.dim = int(pages), int(heads), int(dim)
         self.k = torch.zeros((pages, heads, PAGE, dim), dtype=torch.uint8, device=device)
         self.v = torch.zeros_like(self.k)
@@ -797,6 +806,7 @@ def context_append(plan: ContextPlan, cache: ContextCache, k, v, rope: RopeFrequ
 
 def context_workspace_size(rows: int, q_heads: int, kv_heads: int, dim: int) -> int:
     """Bytes of workspace ``context_attention`` needs on the current device (0 if invalid)."""
+    _need_int32(rows=rows, q_heads=q_heads, kv_heads=kv_heads, dim=dim)
     return int(lib().dg_context_workspace_size(rows, q_heads, kv_heads, dim))
 
 
@@ -839,7 +849,8 @@ def context_attention(plan: ContextPlan, cache: ContextCache, q, out, ws: Contex
     _need(lse is None or (lse.dtype == torch.float32 and lse.dim() == 2 and lse.shape[0] >= plan.rows and
                           lse.shape[1] == heads and lse.is_contiguous() and lse.device == dev),
           "lse must be a contiguous float32 tensor [rows, heads] on the plan's device")
-    _need(scale is None or scale > 0, "scale must be positive")
+    _need(scale is None or np.float32(scale) > 0, "scale must be positive, in 32 bits too (0 would stand for the default)")
+    _need_int32(window=window, max_new=max_new)
     _call(dev, lib().dg_context_attention, "dg_context_attention", stream, plan._ref, cache._ref, ctypes.byref(a),
           ctypes.byref(b), heads, 0.0 if scale is None else scale, None if causal is None else causal.data_ptr(),
           window, max_new, None if lse is None else lse.data_ptr(), ws.buf.data_ptr(), ws.nbytes)
