@@ -167,7 +167,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     // all lanes; only page n of the looked up ones
     auto copy = [&](const CUtensorMap* map, uint8_t* to, uint32_t bar, int n) {
       const int y = (__shfl_sync(0xffffffffu, id, n & 31) * p.kv_heads + it.h) * DG_PAGE;
-      if (lane == 0) {
+      if (lane == 0 && ok) {
         mbar_arrive_expect_tx(bar, Cfg::kPageBytes);
         tma_load_2d(smem_u32(to), map, bar, 0, y, policy);
       }
@@ -399,7 +399,7 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
         copy(&tmK, k_page, k_bar, n + 1);
       }
       if (more) copy(&tmV, v_page, v_bar, n + 1);
-      phase ^= 1u;
+      if (ok) phase ^= 1u;
     }
 
     // the warps meet: (m, l, o) of each through shared memory (the ring is
@@ -532,7 +532,15 @@ attention_rows_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_cons
     __syncthreads();
     pos += seg;
   }
-  if (!ok && lane == 0) atomicOr(p.err, kErrWaitContext);
+  if (!ok && lane == 0) {
+    // It gave up waiting, and has asked for no more pages since.  What it had
+    // asked for (keys of this phase, or of the next where these came; values of
+    // this one) gets another time to land before the block goes.
+    mbar_wait_bounded(k_bar, phase, p.wait_ns);
+    mbar_wait_bounded(v_bar, phase, p.wait_ns);
+    mbar_wait_bounded(k_bar, phase ^ 1u, p.wait_ns);
+  }
+  if (!ok) atomicOr(p.err, kErrWaitContext);
 }
 
 template <int kDim, int kNt>
