@@ -552,7 +552,8 @@ def generate_blocks_context(plan: ContextPlan, E, hidden_fn, n_blocks: int, h_bu
     committed, h_buf)`` is called once more, with the finished canvas, to encode
     it: what it appends then is what the next plan commits (``h_buf`` is not
     read).  DGError 10 when a block does not fit, 9 when a key or value that is
-    not finite was appended."""
+    not finite was appended; a block that was not finished is dropped from the
+    context."""
     import torch
     given = dict(E=E, h_buf=h_buf, blocks=blocks, canvas=canvas, prev_argmax=prev_argmax, accept=accept, entropy=entropy,
                  sampled=sampled, argmax=argmax, stop=stop, workspace=ws.buf, e_scale=e_scale)

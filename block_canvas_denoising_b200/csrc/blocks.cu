@@ -83,6 +83,16 @@ extern "C" dg_status dg_init_canvas(const dg_shape* shape, const dg_params* para
 
 namespace {
 
+// Every request of the batch adds n tokens: the lengths a plan of the driver's
+// reads.  The copy from host memory is staged by the runtime before the call
+// returns.
+dg_status set_lengths(int32_t* add, int B, int32_t n, cudaStream_t cs) {
+  int32_t each[DG_MAX_B];
+  for (int b = 0; b < B; ++b) each[b] = n;
+  return cuda_ok(cudaMemcpyAsync(add, each, sizeof(int32_t) * B, cudaMemcpyHostToDevice, cs), "block lengths") ? DG_OK
+                                                                                                               : DG_ERR_CUDA;
+}
+
 dg_status run_blocks(const dg_shape* shape, const dg_params* params, const void* E, const float* e_scale,
                      int32_t n_blocks, dg_block_hidden_fn hidden_fn, void* user, const dg_context* ctx, int32_t* add,
                      void* h_buf, int32_t* blocks, int32_t* steps_taken, int32_t* canvas, int32_t* prev_argmax,
@@ -101,15 +111,12 @@ dg_status run_blocks(const dg_shape* shape, const dg_params* params, const void*
     if (ctx->B != B || static_cast<size_t>(ctx->rows) < rows) return DG_ERR_UNSUPPORTED_SHAPE;
     if (add == nullptr) return DG_ERR_INVALID_ARG;
     if (device_sms() <= 0) return DG_ERR_NO_DEVICE;
-    // every request adds its canvas; the copy from host memory is staged by
-    // the runtime before the call returns
-    int32_t slots[DG_MAX_B];
-    for (int b = 0; b < B; ++b) slots[b] = shape->L;
-    if (!cuda_ok(cudaMemcpyAsync(add, slots, sizeof(int32_t) * B, cudaMemcpyHostToDevice, cs), "block lengths"))
-      return DG_ERR_CUDA;
+    if ((st = set_lengths(add, B, shape->L, cs)) != DG_OK) return st;
   }
   uint8_t has_prev[DG_MAX_B];
-  for (int32_t j = 0; j < n_blocks; ++j) {
+  bool open = false;  // the context holds slots of a block that is not finished
+  auto block = [&](int32_t j) -> dg_status {
+    dg_status st;
     dg_params pj = *params;
     pj.block = params->block + j;
     if ((st = dg_init_canvas(shape, &pj, canvas, stream)) != DG_OK) return st;
@@ -117,7 +124,9 @@ dg_status run_blocks(const dg_shape* shape, const dg_params* params, const void*
       // the block before (or the prompts) joins the context, this block's
       // slots open behind it
       if ((st = dg_context_plan(ctx, add, nullptr, 1, stream)) != DG_OK) return st;
-      if ((st = dg_context_status(ctx, stream)) != DG_OK) return st;
+      st = dg_context_status(ctx, stream);
+      open = st != DG_ERR_CAPACITY;  // a refused batch has no slots
+      if (st != DG_OK) return st;
     }
     memset(has_prev, 0, sizeof(has_prev));
     BlockCall call{hidden_fn, user, j, j > 0 ? blocks : nullptr, ctx, add, DG_OK};
@@ -130,13 +139,24 @@ dg_status run_blocks(const dg_shape* shape, const dg_params* params, const void*
     if (cudaMemcpyAsync(blocks + static_cast<size_t>(j) * rows, canvas, sizeof(int32_t) * rows,
                         cudaMemcpyDeviceToDevice, cs) != cudaSuccess)
       return DG_ERR_CUDA;
+    if (ctx == nullptr) return DG_OK;
     // encode: the slots hold what the last step's callback appended for the
     // canvas that step started from; the finished canvas goes over it while
     // the batch is still provisional
-    if (ctx != nullptr && block_trampoline(params->max_steps, canvas, h_buf, &call, stream) != 0)
+    if (block_trampoline(params->max_steps, canvas, h_buf, &call, stream) != 0)
       return call.status != DG_OK ? call.status : DG_ERR_CALLBACK;
     // a key or value of this block that is not finite, before anything commits it
-    if (ctx != nullptr && (st = dg_context_status(ctx, stream)) != DG_OK) return st;
+    if ((st = dg_context_status(ctx, stream)) != DG_OK) return st;
+    open = false;
+    return DG_OK;
+  };
+  for (int32_t j = 0; j < n_blocks; ++j) {
+    if ((st = block(j)) == DG_OK) continue;
+    // A block that was not finished leaves no slots behind: the next plan that
+    // commits would make them tokens.
+    if (open && set_lengths(add, B, 0, cs) == DG_OK && dg_context_plan(ctx, add, nullptr, 0, stream) == DG_OK)
+      cudaStreamSynchronize(cs);
+    return st;
   }
   if (cudaStreamSynchronize(cs) != cudaSuccess) return DG_ERR_CUDA;
   return DG_OK;

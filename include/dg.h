@@ -566,8 +566,9 @@ dg_status dg_context_attention(const dg_context* ctx, const dg_context_cache* ca
  * provisional.
  * DG_ERR_CAPACITY when a block does not fit; DG_ERR_VALUE when a key or value
  * that is not finite was appended: by the prompts (before block 0's first step)
- * or during a block (after its encoding: the block is in `blocks`, and not
- * committed to the context). */
+ * or during a block (after its encoding: the block is in `blocks`).  When the
+ * call fails, whatever for, the slots of the block it was at are dropped, and
+ * the context holds the blocks before it. */
 dg_status dg_generate_blocks_context(const dg_shape* shape, const dg_params* params, const void* E,
                                      const float* e_scale, int32_t n_blocks, dg_block_hidden_fn hidden_fn,
                                      void* user, const dg_context* ctx, int32_t* add, void* h_buf,

@@ -132,3 +132,56 @@ def test_an_encoding_that_fails_ends_the_generation():
     assert err.value.code == 7 and isinstance(err.value.__cause__, ValueError)
     assert seen == [(0, 0), (0, 1), (0, 2), (0, 3)]
     assert plan.held.cpu().tolist() == [0, 0]  # nothing of the block was committed
+
+
+@pytest.mark.parametrize("where", [(0, 0), (1, 2), (1, 3), "workspace"])
+def test_a_block_that_was_not_finished_leaves_no_slots(where):
+    # the generation fails in a step, in an encoding, or before its first step; the next one goes on behind the
+    # blocks that were finished, not behind slots that nobody encoded
+    E_bits = synth.embedder_normal(V, D, seed=1)
+    E = to_dev_bf16(E_bits)
+    plan, layer = dg.ContextPlan(B, B * L, 60, 20), Layer(60, 1)
+    prompts = [100, 7]
+    dg.context_plan(plan, ints(prompts))
+    prompt = torch.randint(0, V, (sum(prompts),), device="cuda", dtype=torch.int32)
+    layer(plan, prompt, True)
+    params, fail, seen = dg.Params(max_steps=3), [True], []
+
+    def hidden(j, k, canvas, committed, h):
+        if fail[0] and (j, k) == where:
+            raise ValueError("stop")
+        seen.append(plan.held.cpu().tolist())
+        layer(plan, canvas, k == params.max_steps)
+        h.copy_(to_dev_bf16(synth.loop_hidden(k, synth.loop_targets(L, V, seed=3, B=B), E_bits, seed=4)))
+    R = B * L
+    i32 = lambda *n: torch.zeros(n, dtype=torch.int32, device="cuda")  # noqa: E731
+    blocks, ws = i32(2, R), dg.Workspace(B, D, V)
+
+    def run():
+        dg.generate_blocks_context(
+            plan, E, hidden, 2, torch.zeros((R, D), dtype=torch.bfloat16, device="cuda"), blocks, i32(R), i32(R),
+            torch.zeros(R, dtype=torch.uint8, device="cuda"), torch.zeros(R, dtype=torch.float32, device="cuda"), i32(R), i32(R),
+            i32(B), ws, params)
+    nbytes = ws.nbytes
+    if where == "workspace":
+        ws.nbytes = 64
+    with pytest.raises(dg.DGError) as err:
+        run()
+    assert err.value.code == (3 if where == "workspace" else 7)
+    done = 0 if where == "workspace" else where[0]
+    held = [p + done * L for p in prompts]
+    assert plan.held.cpu().tolist() == held and plan.lens.cpu().tolist() == held
+    finished = blocks[:done].clone()
+    ws.nbytes, fail[0] = nbytes, False
+    seen.clear()
+    run()
+    assert seen[0] == held and plan.lens.cpu().tolist() == [n + 2 * L for n in held]
+    ref, by_hand = dg.ContextPlan(B, B * L, 60, 20), Layer(60, 1)
+    dg.context_plan(ref, ints(prompts))
+    by_hand(ref, prompt, True)
+    for tokens in (*finished, *blocks):
+        dg.context_plan(ref, ints([L] * B), commit=True)
+        by_hand(ref, tokens, True)
+    for x, y in zip(held_values(plan, layer, plan.lens.tolist()), held_values(ref, by_hand, ref.lens.tolist())):
+        assert np.array_equal(x, y)
+    assert dg.context_status(plan) == 0
