@@ -271,24 +271,23 @@ DG_DEV void unit_chunks(int u, int rot16, bool interleaved, int& ca, int& cb) {
   ca = halves ? u : 2 * u;
   cb = halves ? u + rot16 : 2 * u + 1;
 }
+// (x, y) turned.  Its roundings are spelled out, so that a number is the same
+// wherever this is inlined.
+DG_DEV void rotate_pair(float& x, float& y, const float2& t) {
+  const float a = x, b = y;
+  x = __fmaf_rn(a, t.x, -__fmul_rn(b, t.y));
+  y = __fmaf_rn(a, t.y, __fmul_rn(b, t.x));
+}
 DG_DEV void rotate_unit(float (&a)[8], float (&b)[8], const float2 (&t)[8], bool interleaved) {
   if (interleaved) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const float x = a[2 * i], y = a[2 * i + 1];
-      a[2 * i] = x * t[i].x - y * t[i].y;
-      a[2 * i + 1] = x * t[i].y + y * t[i].x;
-      const float z = b[2 * i], w = b[2 * i + 1];
-      b[2 * i] = z * t[4 + i].x - w * t[4 + i].y;
-      b[2 * i + 1] = z * t[4 + i].y + w * t[4 + i].x;
+      rotate_pair(a[2 * i], a[2 * i + 1], t[i]);
+      rotate_pair(b[2 * i], b[2 * i + 1], t[4 + i]);
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = a[i], y = b[i];
-      a[i] = x * t[i].x - y * t[i].y;
-      b[i] = x * t[i].y + y * t[i].x;
-    }
+    for (int i = 0; i < 8; ++i) rotate_pair(a[i], b[i], t[i]);
   }
 }
 

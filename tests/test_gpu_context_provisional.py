@@ -196,3 +196,33 @@ def test_planned_over_in_a_graph():
         graph.replay()
         check(plan, cache, append_to(held, plan, x, heads))
     assert dg.context_status(plan) == 0
+
+
+@pytest.mark.parametrize("dim,heads,rot,il", [(128, 2, 128, False), (64, 9, 48, True), (128, 20, 64, False)])
+def test_rotated_keys_are_the_same_behind_a_batch_planned_over(dim, heads, rot, il):
+    # the rows' codes too, to the last bit: whether a head's scale was to be taken back or not
+    rng = np.random.default_rng(8)
+    f = dg.RopeFrequencies(rot, interleaved=il)
+    B, rows = 5, 220
+    held, add = [37, 100, 1, 63, 130], [40, 30, 64, 1, 20]
+    prompt = rows_of(rng, sum(held), heads, dim, 0.01)
+    x, large = rows_of(rng, rows, heads, dim, 1.0), rows_of(rng, rows, heads, dim, 300.0)
+    got = []
+    for batches in ((x,), (large, x), (large, large, x), (x, large, x)):
+        plan, cache = dg.ContextPlan(B, max(rows, sum(held)), 40, 6), dg.ContextCache(40, heads, dim)
+        dg.context_plan(plan, ints(held))
+        p = torch.zeros((plan.rows, 2 * heads, dim), dtype=torch.bfloat16, device="cuda")
+        p[:sum(held)] = prompt
+        dg.context_append(plan, cache, p[:, :heads], p[:, heads:], rope=f)
+        for i, b in enumerate(batches):
+            dg.context_plan(plan, ints(add), commit=i == 0)
+            p[:rows] = b
+            dg.context_append(plan, cache, p[:, :heads], p[:, heads:], rope=f)
+        state = []
+        for r, n in enumerate(plan.lens.cpu().tolist()):
+            page = plan.table[r, :-(-n // 64)].long()
+            for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)):
+                state += [c[page].transpose(1, 2).reshape(-1, heads, dim)[:n], s[page]]
+        got.append(state)
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
