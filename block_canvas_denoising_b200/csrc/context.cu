@@ -78,8 +78,9 @@ DG_DEV int owner_of(const int* start, int B, int i) {
 // stack, the table) and the two cluster barriers that keep every read of the
 // old state before the first write of the new one; one launch with barriers
 // in hardware instead of three launches in a row.  8 requests x 256 rows take
-// 4.4 us, 256 requests x up to 300 rows with some leaving 8.7 us (18.7 with a
-// search per row instead of per run).
+// 4.5 us in a graph of their own and 3.0 one after another, 256 requests x up to
+// 300 rows with some leaving 8.6 and 6.8 (18.7 with a search per row instead of
+// per run).
 __global__ void __cluster_dims__(kPlanCtas, 1, 1) __launch_bounds__(kPlanThreads)
 context_plan_kernel(const dg_context c, const int32_t* __restrict__ add, const uint8_t* __restrict__ release,
                     int32_t commit) {
@@ -310,8 +311,8 @@ constexpr int kRopeThreads = 256;
 // shared memory; the heads then stream through, 32 bytes a thread, a thread
 // staying on its unit and walking the (token, head) pairs by a fixed stride
 // (256 threads / units = step_tokens * heads + step_heads) without a division.
-// Bound by memory: 67 MB of 8191 rows x 16 heads x 128 take 13.1 us from HBM,
-// 5.1 TB/s, 0.78 of a plain copy's rate.
+// Bound by memory: 67 MB of 8191 rows x 16 heads x 128 take 13.4 us from HBM,
+// 5.0 TB/s, 0.76 of a plain copy's rate (12.6 us with the input in L2).
 template <int kDim, int kTokens>
 __global__ void __launch_bounds__(kRopeThreads)
 rope_kernel(const uint8_t* x, uint8_t* out, int64_t xr, int64_t xh, int64_t outr, int64_t outh, int rows, int heads,
@@ -672,10 +673,12 @@ __device__ __noinline__ void append_grown(const dg_context& c, const dg_context_
 // the two things that need them, the largest magnitude and the codes, and the
 // next head's are on their way meanwhile.  The turns of the run's tokens are
 // formed once and serve all of its heads.
-// Measured (8 heads x 128): 32 requests x 256 rows, 50 MB, in 12.3 us, 4.1 TB/s,
-// bound by latency at two blocks an SM (116 registers a thread; squeezed to 78
-// and 64 for three and four blocks: 17.6 and 23.5 us); 32 requests x 1 row in
-// 3.6 us.
+// Measured (8 heads x 128): 32 requests x 256 rows, 50 MB, in 17.9 us from HBM,
+// 2.8 TB/s, and 12.4 one after another with the rows in L2; bound by latency at
+// two blocks an SM (105 registers a thread; squeezed to 78 and 64 for three and
+// four blocks it took 17.6 and 23.5 us where two took 12.3, in L2); 32 requests x
+// 1 row in 3.5 us.  Behind a plan that had another batch raise every scale of
+// its pages, 32 x 256 rows take 22 us, 32 x 1 row 11.
 template <int kDim>
 __global__ void __launch_bounds__(kAppendThreads<kDim>)
 context_append_kernel(const __grid_constant__ dg_context c, const __grid_constant__ dg_context_cache cache,
@@ -990,8 +993,9 @@ dg_status dg_context_append(const dg_context* ctx, const dg_context_cache* cache
   const dg_rope_args none = {};
   // More heads a CTA save turns and starts, until too few CTAs are left to
   // fill the device: up to 3.5 an SM.  1 / 2 / 4 / 8 heads a CTA, in us (8 heads
-  // x 128): 32 requests x 1 row 4.5 / 3.6 / 4.4 / 5.6; 4 x 256 rows 4.5 / 5.2 /
-  // 5.4 / 8.0; 16 x 256 11.8 / 9.3 / 8.3 / 10.7; 32 x 256 19.9 / 14.8 / 12.8 / 12.2.
+  // x 128, one after another): 32 requests x 1 row 4.5 / 3.6 / 4.4 / 5.7; 4 x 256
+  // rows 4.2 / 5.1 / 6.0 / 7.9; 16 x 256 12.3 / 9.7 / 8.0 / 11.2; 32 x 256 20.9 /
+  // 15.3 / 13.0 / 11.9.
   const int runs = DG_CONTEXT_RUNS(ctx->rows, ctx->B);
   int per = 1;
   while (per < cache->heads && per < kAppendHeads && 4ll * runs * ((cache->heads + per - 1) / per) > 7ll * sms) per *= 2;

@@ -92,7 +92,7 @@ DG_DEV uint32_t transpose8(uint32_t v) {
 // of a value, so operands are whole 16-byte reads of the codes as the cache
 // holds them.  Between the products P is transposed 8 x 8 at a time.
 // Measured (128-wide heads): one token of 32 requests over 1000 to 9000 tokens
-// (8 kv heads, 4 query heads each) in 61.5 us, 5.5 TB/s of cache, 0.84 of a plain
+// (8 kv heads, 4 query heads each) in 61.9 us, 5.5 TB/s of cache, 0.84 of a plain
 // copy's rate: bound by HBM.  One token over 4096 (4 kv heads) in 13 us: a
 // chain of some ten dependent reads (lengths, table, scales, page, the other
 // CTAs' parts) of 0.5 to 1 us each.

@@ -17,7 +17,7 @@
 // O is seldom rescaled; weights stay below 2^(kWeightLog2 + 8) = 2^14.
 // Measured (22 heads over 2 kv heads x 128): 32 canvases of 256 rows over 2816
 // to 5376 tokens in 380 us, 960 TFLOP/s at 1.9 GHz (under a sustained load, at
-// the power limit, 413 us), a canvas over 4352 in 33 us; 16 heads over 4, a canvas
+// the power limit, 437 us), a canvas over 4352 in 33 us; 16 heads over 4, a canvas
 // at the end of 131072 tokens, in 264 us, 1.04 PFLOP/s.  A tile takes some
 // 1900 cycles, in which the tensor pipe is busy for 63 %, the special function
 // unit for 38 and the issue slots for 48: what bounds it is the chain of one

@@ -416,7 +416,8 @@ typedef struct {
   int32_t* free_next;  /* [1] free pages once the batch is committed */
   int32_t* status;     /* [2] outcome of the last plan; latch of dg_context_append */
   int32_t* epoch;      /* [1] number of the plan, any value to begin with (contexts that
-                          share a cache: different ones); NULL: see dg_context_cache.kept */
+                          use one cache, one after another: different ones); NULL: see
+                          dg_context_cache.kept */
 } dg_context;
 
 /* dg_context_plan -- block tables and slot maps of a batch, from request
@@ -537,11 +538,16 @@ size_t dg_context_workspace_size(int32_t rows, int32_t q_heads, int32_t kv_heads
  *   window   > 0: a row sees only tokens later than its own minus window
  *            (its own counted: `window` tokens up to itself).  0: no limit.
  *   max_new  the most rows one request of the batch has, when the host knows
- *            it (0: not known): chooses the kernel, never the result's
- *            meaning.
+ *            it (0: not known, taken as ctx->rows): chooses the kernel, never
+ *            the result's meaning.  Single tokens need it: without it a context
+ *            of many rows has them go through the kernel for many.
  *   lse      float [rows][q_heads] or NULL: ln of the sum of exp(logits).
- * Logits and sums are float32.  A row that sees no token gives 0 (lse -inf).  A query that is not finite
- * gives NaN in its own row and head only.  Cache codes must not be NaN
+ * Logits and sums are float32, weights float16 (up to 2^14, 11 bits).  Up to 32
+ * rows per kv head and request (by max_new) queries enter as they are; with more
+ * they enter as two E4M3 terms: exact down to 2^-9 of the row's largest element,
+ * and off by at most 2^-17 of that below, so a row's last bits can depend on
+ * which of the two it is.  A row that sees no token gives 0 (lse -inf).  A query
+ * that is not finite gives NaN in its own row and head only, where it sees a token.  Cache codes must not be NaN
  * (dg_context_append stores none); tokens on a page outside the pool are not
  * seen.  Rows from start[B] on are left as they were.  Results do not depend
  * on timing: splits and their joining follow the lengths alone.  Calls that
