@@ -430,7 +430,8 @@ DG_DEV uint2 e4m3_chunk(const float (&x)[8], float inv) {
 // page, which tokens and which plan they are, and what the append left in the
 // page.  The next plan's append begins with them if the page is still that.  A
 // mark beside each scale says in which plan and behind how many tokens it has
-// grown, 0 if it has not: all that an append reads where nothing is to be done.
+// grown, 0 if it has not since the page was begun: all that an append reads
+// where nothing is to be done.
 // (With every head's tag read in any case, 32 requests x 8 heads x 1 row took
 // 3.8 us instead of 3.5.)
 struct KeptTag {
@@ -443,6 +444,9 @@ struct KeptTag {
 static_assert(sizeof(KeptTag) == 32, "two 16-byte words");
 DG_DEV uint32_t grown_mark(uint32_t epoch, int off) { return epoch << 6 | static_cast<uint32_t>(off); }  // off < DG_PAGE
 // dg_context_cache.kept: marks [k, v][pages][heads], tags and codes [slots][k, v][heads].
+DG_DEV uint32_t* kept_marks(const dg_context_cache& cache, bool is_k) {
+  return reinterpret_cast<uint32_t*>(cache.kept) + (is_k ? 0 : static_cast<size_t>(cache.pages) * cache.heads);
+}
 struct KeptLayout {
   int slots;
   size_t tags, codes, total;
@@ -542,7 +546,8 @@ DG_DEV void append_grown_head(const dg_context_cache& cache, const dg_heads& in,
   bool mine = false, restore = false;  // the tag is of this page as it stands: of this plan's batch, or of another's
   float base = old;
   uint32_t a = 0, b = 0;
-  if (tag != nullptr && tag->page == page && tag->off == off && __float_as_uint(tag->grown) == __float_as_uint(old)) {
+  if (tag != nullptr && tag->page == page && tag->off == off && __float_as_uint(tag->grown) == __float_as_uint(old) &&
+      marks[at] == grown_mark(tag->epoch, off)) {
     for (int i0 = t; i0 < words; i0 += kAtOnce * kTeam) {
       uint32_t w[kAtOnce];
 #pragma unroll
@@ -657,7 +662,7 @@ __device__ __noinline__ void append_grown(const dg_context& c, const dg_context_
                                           const float2 (*turns)[kDim / 2], int rot16, bool il, bool is_k, int4 run,
                                           const GrownHead* list, int count, uint32_t* sums) {
   const KeptPlace k = kept_place<kDim>(c, cache, is_k, run.x, run.y, sums);
-  uint32_t* marks = reinterpret_cast<uint32_t*>(cache.kept) + (is_k ? 0 : static_cast<size_t>(cache.pages) * cache.heads);
+  uint32_t* marks = kept_marks(cache, is_k);
   if (count <= 2) {
     for (int i = 0; i < count; ++i)
       append_grown_head<kDim, true>(cache, in, marks, turns, rot16, il, is_k, run, list[i].head, list[i].want, k, sums);
@@ -722,12 +727,17 @@ context_append_kernel(const __grid_constant__ dg_context c, const __grid_constan
     }
   };
   load(src);
-  // heads whose scale another plan's batch behind the same tokens has made to grow
+  // Heads whose scale another plan's batch behind the same tokens has made to
+  // grow.  A page that is begun has not grown.
   bool grown = false;
-  if (off > 0 && static_cast<int>(threadIdx.x) < heads && cache.kept != nullptr && c.epoch != nullptr) {
-    const uint32_t* marks = reinterpret_cast<const uint32_t*>(cache.kept) + (is_k ? 0 : static_cast<size_t>(cache.pages) * cache.heads);
-    const uint32_t m = marks[at0 + threadIdx.x], now = grown_mark(static_cast<uint32_t>(*c.epoch), off);
-    grown = m != now && (m & (DG_PAGE - 1)) == (now & (DG_PAGE - 1));
+  if (static_cast<int>(threadIdx.x) < heads && cache.kept != nullptr && c.epoch != nullptr) {
+    uint32_t* mark = kept_marks(cache, is_k) + at0 + threadIdx.x;
+    if (off > 0) {
+      const uint32_t m = *mark, now = grown_mark(static_cast<uint32_t>(*c.epoch), off);
+      grown = m != now && (m & (DG_PAGE - 1)) == (now & (DG_PAGE - 1));
+    } else {
+      *mark = 0;
+    }
   }
   int later = 0;  // heads for append_grown
   if (rot16 > 0) {

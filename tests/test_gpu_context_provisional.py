@@ -226,3 +226,29 @@ def test_rotated_keys_are_the_same_behind_a_batch_planned_over(dim, heads, rot, 
         got.append(state)
     for other in got[1:]:
         assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
+@pytest.mark.parametrize("pages", [4, 300])
+def test_a_page_that_is_begun_again_has_nothing_of_before(pages):
+    # a request's tokens, all but 0 beside a later batch, and the next one's on the same page, all 0 under the same
+    # scale: nothing tells the two pages' codes apart
+    heads, dim = 2, 64
+    plan, cache = dg.ContextPlan(1, 64, pages, 4), dg.ContextCache(pages, heads, dim)
+    x = torch.full((64, 2 * heads, dim), 1e-6, dtype=torch.bfloat16, device="cuda")
+    dg.context_plan(plan, ints([20]))
+    run(plan, cache, x, heads)
+    x.fill_(400.0)
+    dg.context_plan(plan, ints([5]), commit=True)
+    run(plan, cache, x, heads)
+    page = int(plan.table[0, 0])
+    assert cache.k_scale[page].tolist() == [1.0] * heads and int(cache.k[page, :, :20].max()) == 0
+    dg.context_plan(plan, ints([20]), release=ints([1], torch.uint8))
+    assert int(plan.table[0, 0]) == page
+    x.zero_()
+    run(plan, cache, x, heads)
+    x.fill_(0.01)
+    dg.context_plan(plan, ints([5]), commit=True)
+    want = append_to(state_of(cache), plan, x, heads)
+    run(plan, cache, x, heads)
+    check(plan, cache, want)
+    assert int(cache.k[page, :, :20].max()) == 0 and cache.k_scale[page].tolist() == [1.0] * heads
