@@ -691,7 +691,8 @@ class ContextPlan:
         self.runs = zeros(rows // PAGE + 2 * B, 4)
         self.runs[:, 0] = -1
         self.status = zeros(2)
-        self.epoch = zeros(1) + next(_plans) * 0x9E3779B1 % 2 ** 31  # plans that share a cache start far apart
+        # plans that use one cache start far apart
+        self.epoch = torch.full((1,), next(_plans) * 0x9E3779B1 % 2 ** 31, dtype=torch.int32, device=device)
         self.add = zeros(B)  # lengths of generate_blocks_context
         self._c = _Context(B, rows, pages, max_pages, *(getattr(self, n).data_ptr() for n in (
             "table", "held", "free_list", "free_count", "lens", "start", "positions", "slots", "runs", "free_next",

@@ -439,9 +439,7 @@ struct KeptTag {
   uint32_t epoch;       // the plan whose batch made the scale grow
   float base, grown;    // scales before and after
   uint32_t check[2];    // sums over the codes as rounded again
-  uint32_t unused;
 };
-static_assert(sizeof(KeptTag) == 32, "two 16-byte words");
 DG_DEV uint32_t grown_mark(uint32_t epoch, int off) { return epoch << 6 | static_cast<uint32_t>(off); }  // off < DG_PAGE
 // dg_context_cache.kept: marks [k, v][pages][heads], tags and codes [slots][k, v][heads].
 DG_DEV uint32_t* kept_marks(const dg_context_cache& cache, bool is_k) {
@@ -525,8 +523,9 @@ DG_DEV KeptPlace kept_place(const dg_context& c, const dg_context_cache& cache, 
 // held codes under the scale that comes of it, that scale, and the rows' codes.
 // By a block, or (kBlock false) by a warp.
 template <int kDim, bool kBlock>
-DG_DEV void append_grown_head(const dg_context_cache& cache, const dg_heads& in, uint32_t* marks, const float2 (*turns)[kDim / 2], int rot16,
-                              bool il, bool is_k, int4 run, int h, float s, const KeptPlace& k, uint32_t* sums) {
+DG_DEV void append_grown_head(const dg_context_cache& cache, const dg_heads& in, uint32_t* marks,
+                              const float2 (*turns)[kDim / 2], int rot16, bool il, bool is_k, int4 run, int h, float s,
+                              const KeptPlace& k, uint32_t* sums) {
   constexpr int kUnits = kDim / 16, kTeam = kBlock ? kAppendThreads<kDim> : 32;
   constexpr int kAtOnce = 8;  // words on their way: all that a block has of a page
   const int t = kBlock ? threadIdx.x : (threadIdx.x & 31);

@@ -19,7 +19,7 @@ def test_kept_size(libdg):
     # a word beside each scale; a page's codes of each head, keys and values, and a tag for each, of at most 256 pages
     for pages, heads, dim, slots in ((1, 1, 64, 1), (40, 3, 128, 40), (256, 8, 128, 256), (70000, 8, 128, 256), (1 << 24, 1024, 64, 256)):
         n = libdg.dg_context_kept_size(pages, heads, dim)
-        assert 0 <= n - pages * 2 * heads * 4 - slots * 2 * heads * (64 * dim + 32) < 512
+        assert 0 <= n - pages * 2 * heads * 4 - slots * 2 * heads * (64 * dim + 28) < 512
     for bad in ((0, 1, 64), (1, 0, 64), (1, 1025, 64), (1, 1, 96), ((1 << 24) + 1, 1, 64)):
         assert libdg.dg_context_kept_size(*bad) == 0
 
